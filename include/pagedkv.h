@@ -2,7 +2,7 @@
  * pagedkv.h -- C ABI of the B200 (sm_100a) paged-KV attention library
  * (libpagedkv.so).
  *
- * Three operations, all enqueued on the caller's CUDA stream:
+ * Operations, all enqueued on the caller's CUDA stream; the three of the path:
  *
  *   pkv_kv_append          write new K/V tokens into cache blocks;
  *   pkv_paged_decode_attn  attention of one or a few query tokens against a
@@ -105,6 +105,8 @@ extern "C" {
                                     from max_seqlen_k, so keys past its last split (key
                                     tile) are not read and the result is not that
                                     context's attention */
+#define PKV_DEVERR_SCALE 32      /* a scale byte of the 8-bit cache outside [64, 190]: the
+                                    nearest byte in range was used */
 
 /*
  * pkv_kv_append: for every sequence b and new token t < n_new, copy the bf16
@@ -408,6 +410,154 @@ int pkv_paged_prefill_attn_bwd(const void *q, const int64_t q_strides[3],
 
 /* Workspace bytes pkv_paged_prefill_attn_bwd needs (0 on invalid arguments). */
 size_t pkv_bwd_workspace_size(int batch, int seqlen_q, int Hq);
+
+/*
+ * Rotary positions.  A row of head_dim elements at position p has its first
+ * rotary_dim elements turned pair by pair: pair i by theta = p * inv_freq[i],
+ *   y1 = x1 c - x2 s,  y2 = x2 c + x1 s,  c = mscale cos theta, s = mscale sin theta,
+ * with (x1, x2) the elements (i, i + rotary_dim / 2), or (2i, 2i + 1) when
+ * interleaved; the other elements are copied.  theta is formed and reduced in
+ * fp64 from the fp32 frequencies, the rest is fp32, and y is rounded to bf16
+ * once.  Frequencies stretched for a long context are the caller's table;
+ * mscale is the magnitude factor that goes with one (1 otherwise).
+ *   inv_freq     device fp32 [rotary_dim / 2]
+ *   rotary_dim   a multiple of 16, at most head_dim
+ *   mscale       > 0
+ */
+typedef struct pkv_rope_params {
+  const float *inv_freq;
+  int rotary_dim;
+  int interleaved;
+  float mscale;
+} pkv_rope_params;
+
+/*
+ * pkv_rope: q [batch, n, Hq, D] to q_out and, unless k and k_out are null,
+ * k [batch, n, Hk, D] to k_out (bf16, element strides (b, s, h)), row (b, i) at
+ * positions[b * n + i] (device int32, any sign).  Packed tokens: batch = 1.
+ * An output may be its input; it must not overlap it otherwise.  inverse != 0
+ * applies the transpose (s negated): the gradient of the forward call, given
+ * the gradient of its output.  batch or n 0 does nothing.
+ */
+int pkv_rope(const void *q, const int64_t q_strides[3], void *q_out, const int64_t qo_strides[3], int Hq,
+             const void *k, const int64_t k_strides[3], void *k_out, const int64_t ko_strides[3], int Hk,
+             const int32_t *positions, int batch, int n, int D, const pkv_rope_params *rope, int inverse,
+             void *stream);
+
+/*
+ * pkv_kv_append_rope: pkv_kv_append with the rotation applied on the way.  New
+ * token t of sequence b is at position seqlens[b] + t (seqlens BEFORE the
+ * append); its key is rotated there and stored, its value stored unchanged,
+ * and, unless q and q_out are null, its query row q [.., Hq, D] is rotated to
+ * q_out (which may be q).  The tokens are dense, [batch, n_new, heads, D] with
+ * strides (batch, token, head), when cu_seqlens_new is null (total_new unused);
+ * otherwise packed, [total_new, heads, D] with the last two of the strides
+ * used, sequence b owning cu_seqlens_new[b] .. cu_seqlens_new[b+1] - 1.  Tokens
+ * behind cu_seqlens_new[batch] are left alone.  Two sequences must not share a
+ * block that the call writes.  Errors and device error bits as pkv_kv_append;
+ * a range of cu_seqlens_new that decreases or leaves [0, total_new] sets
+ * PKV_DEVERR_QUERY_LEN and is skipped.
+ */
+int pkv_kv_append_rope(const void *q, const int64_t q_strides[3], void *q_out, const int64_t qo_strides[3],
+                       int Hq, const void *k_new, const int64_t kn_strides[3], const void *v_new,
+                       const int64_t vn_strides[3], const int32_t *cu_seqlens_new, int total_new,
+                       void *k_cache, const int64_t k_strides[3], void *v_cache, const int64_t v_strides[3],
+                       int64_t num_blocks, const int32_t *block_table, int64_t bt_stride,
+                       int max_blocks_per_seq, const int32_t *seqlens, int batch, int n_new, int Hkv, int D,
+                       int block_size, const pkv_rope_params *rope, int32_t *err, void *stream);
+
+/*
+ * pkv_kv_append_rope_bwd: the gradients of pkv_kv_append_rope's inputs from
+ * those of its outputs: dq = the transposed rotation of dq_rot (unless both
+ * are null), dk_new = that of the rows of dk_cache at the new tokens'
+ * positions, dv_new = those rows of dv_cache.  dk_cache / dv_cache are
+ * gradient buffers laid out like the caches (pkv_paged_prefill_attn_bwd's);
+ * seqlens, tokens and errors as in the forward call (seqlens BEFORE the
+ * append).  A token whose block cannot be read gets zeros.
+ */
+int pkv_kv_append_rope_bwd(const void *dq_rot, const int64_t dqr_strides[3], void *dq,
+                           const int64_t dq_strides[3], int Hq, const void *dk_cache,
+                           const int64_t dkc_strides[3], const void *dv_cache, const int64_t dvc_strides[3],
+                           void *dk_new, const int64_t dkn_strides[3], void *dv_new,
+                           const int64_t dvn_strides[3], const int32_t *cu_seqlens_new, int total_new,
+                           int64_t num_blocks, const int32_t *block_table, int64_t bt_stride,
+                           int max_blocks_per_seq, const int32_t *seqlens, int batch, int n_new, int Hkv,
+                           int D, int block_size, const pkv_rope_params *rope, int32_t *err, void *stream);
+
+/*
+ * The 8-bit cache.  K and V are e4m3 bytes, views [num_blocks, block_size, Hkv,
+ * D] with element (= byte) strides that are multiples of 16 and 16-byte aligned
+ * bases.  Every block and KV head has one scale for K and one for V, a power
+ * of two 2^e with e in [-63, 63], held as the byte e + 127 (E8M0), views
+ * [num_blocks, Hkv] with strides (block, head).  A cached value is
+ * e4m3 * 2^e: a bf16 number, exactly.
+ *
+ * pkv_kv_append_q8: as pkv_kv_append_rope into such a cache (rope null: no
+ * rotation, and q / q_out must be null).  For every block and head touched, K
+ * and V each: need = the least e with max |new value| <= 448 * 2^e (K after the
+ * rotation, in fp32; held to [-63, 63]; zeros and non-finite values do not
+ * count).  A block that holds earlier tokens of the sequence (slots before the
+ * first new token's) keeps a larger scale and is requantised to a larger new
+ * one: q' = e4m3(q * 2^(e - e')), which changes no value unless it becomes
+ * subnormal.  A block whose slot 0 is new starts afresh with need.  New values
+ * are e4m3(x * 2^-e), rounded to nearest even once (infinities saturate, NaN
+ * stays NaN).  Slots behind the new tokens are left as they were.
+ */
+int pkv_kv_append_q8(const void *q, const int64_t q_strides[3], void *q_out, const int64_t qo_strides[3],
+                     int Hq, const void *k_new, const int64_t kn_strides[3], const void *v_new,
+                     const int64_t vn_strides[3], const int32_t *cu_seqlens_new, int total_new,
+                     void *k_cache, const int64_t k_strides[3], void *v_cache, const int64_t v_strides[3],
+                     uint8_t *k_scale, const int64_t ks_strides[2], uint8_t *v_scale,
+                     const int64_t vs_strides[2], int64_t num_blocks, const int32_t *block_table,
+                     int64_t bt_stride, int max_blocks_per_seq, const int32_t *seqlens, int batch, int n_new,
+                     int Hkv, int D, int block_size, const pkv_rope_params *rope, int32_t *err,
+                     void *stream);
+
+/*
+ * pkv_paged_decode_attn_q8 / pkv_paged_prefill_attn_q8 / pkv_paged_varlen_attn_q8:
+ * pkv_paged_decode_attn, pkv_paged_prefill_attn and pkv_paged_varlen_attn over
+ * an 8-bit cache: the same arguments with the scale views behind the caches,
+ * the same workspace (pkv_workspace_size, pkv_varlen_workspace_size), masks,
+ * errors and error bits (and PKV_DEVERR_SCALE), the same splits and merge.  0 <
+ * scale <= 8.  q stays bf16 and out bf16: a query row takes part as two 8-bit
+ * operands that add up to it (to 2^-21 of its largest element or exactly; rows
+ * whose largest magnitude is above 2^67 saturate), a probability as three that
+ * add up to its fp16 value; sums and softmax statistics are fp32.  For a given
+ * cache a row's bits depend on its own query and keys alone: not on the batch,
+ * the table, or which of the three calls computed it.
+ */
+int pkv_paged_decode_attn_q8(const void *q, const int64_t q_strides[3], const void *k_cache,
+                             const int64_t k_strides[3], const void *v_cache,
+                             const int64_t v_strides[3], const uint8_t *k_scale,
+                             const int64_t ks_strides[2], const uint8_t *v_scale,
+                             const int64_t vs_strides[2], int64_t num_blocks,
+                             const int32_t *block_table, int64_t bt_stride, int max_blocks_per_seq,
+                             const int32_t *seqlens, int max_seqlen_k, int batch, int seqlen_q,
+                             int Hq, int Hkv, int D, int block_size, float scale, int causal,
+                             void *out, const int64_t out_strides[3], float *lse, void *workspace,
+                             size_t workspace_bytes, int32_t *err, void *stream);
+int pkv_paged_prefill_attn_q8(const void *q, const int64_t q_strides[3], const void *k_cache,
+                              const int64_t k_strides[3], const void *v_cache,
+                              const int64_t v_strides[3], const uint8_t *k_scale,
+                              const int64_t ks_strides[2], const uint8_t *v_scale,
+                              const int64_t vs_strides[2], int64_t num_blocks,
+                              const int32_t *block_table, int64_t bt_stride, int max_blocks_per_seq,
+                              const int32_t *seqlens, int max_seqlen_k, int batch, int seqlen_q,
+                              int Hq, int Hkv, int D, int block_size, float scale, int causal,
+                              void *out, const int64_t out_strides[3], float *lse, void *workspace,
+                              size_t workspace_bytes, int32_t *err, void *stream);
+int pkv_paged_varlen_attn_q8(const void *q, const int64_t q_strides[2], const int32_t *cu_seqlens_q,
+                             int total_q, int max_seqlen_q, const void *k_cache,
+                             const int64_t k_strides[3], const void *v_cache,
+                             const int64_t v_strides[3], const uint8_t *k_scale,
+                             const int64_t ks_strides[2], const uint8_t *v_scale,
+                             const int64_t vs_strides[2], int64_t num_blocks,
+                             const int32_t *block_table, int64_t bt_stride, int max_blocks_per_seq,
+                             const int32_t *seqlens, int max_seqlen_k, int batch, int Hq, int Hkv,
+                             int D, int block_size, float scale, int causal, void *out,
+                             const int64_t out_strides[2], float *lse, void *final_out,
+                             const int64_t final_strides[2], float *final_lse, void *workspace,
+                             size_t workspace_bytes, int32_t *err, void *stream);
 
 /* Workspace bytes the attention calls need: fp32 split partials
  * (m, l, acc[D]) for every (batch, query row, query head, split). */

@@ -25,3 +25,15 @@ from .binding import (  # noqa: F401
     varlen_workspace_size,
     workspace_size,
 )
+from .cache8 import (  # noqa: F401
+    kv_append_q8,
+    paged_decode_attn_q8,
+    paged_prefill_attn_q8,
+    paged_varlen_attn_q8,
+)
+from .rotary import (  # noqa: F401
+    kv_append_rope,
+    kv_append_rope_bwd,
+    rope,
+    rope_frequencies,
+)

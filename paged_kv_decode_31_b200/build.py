@@ -14,11 +14,11 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libpagedkv.so")
-SOURCES = ["pagedkv.cu"]
+SOURCES = ["pagedkv.cu", "pagedkv_q8.cu", "pagedkv_rope.cu"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
-    "-O3", "-lineinfo", "-std=c++17", "-fmad=false",
+    "-t", "0", "-O3", "-lineinfo", "-std=c++17", "-fmad=false",
     "-Xcompiler", "-fPIC", "-shared",
     "--expt-relaxed-constexpr",
 ]

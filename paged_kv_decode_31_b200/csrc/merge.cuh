@@ -118,6 +118,7 @@ __device__ __forceinline__ void merge_row(const MergeParams &p, int64_t row, int
     i = static_cast<int>(tok - a);
     nq = __ldg(p.cu_q + b + 1) - a;
     if (i >= p.seqlen_q) return;  // past the host bound: flagged by the split kernel
+    if (i >= nq) return;          // behind the last sequence: no partial, the row stays as it was
   } else {
     i = static_cast<int>(tok % p.seqlen_q);
     b = static_cast<int>(tok / p.seqlen_q);

@@ -15,6 +15,7 @@
 #include "attn_bwd.cuh"
 #include "attn_rows.cuh"
 #include "attn_split.cuh"
+#include "host.cuh"
 #include "kv_append.cuh"
 #include "merge.cuh"
 
@@ -28,63 +29,7 @@ static_assert(PKV_DEVERR_SEQ_LEN == pkv::kErrSeqLen, "error bits");
 
 namespace {
 
-constexpr int kMaxDevices = 64;
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  });
-  return fn;
-}
-
-int sm_count(int dev) {
-  static std::atomic<int> cache[kMaxDevices];
-  if (dev < 0 || dev >= kMaxDevices) return 148;
-  int v = cache[dev].load(std::memory_order_relaxed);
-  if (v > 0) return v;
-  if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0)
-    v = 148;
-  cache[dev].store(v, std::memory_order_relaxed);
-  return v;
-}
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool pow2_in(int v, int lo, int hi) { return v >= lo && v <= hi && (v & (v - 1)) == 0; }
-
-int log2i(int v) {
-  int s = 0;
-  while ((1 << s) < v) ++s;
-  return s;
-}
-
-// Element strides usable for 128-bit access: positive multiples of 8.
-bool strides_ok(const int64_t *st) {
-  if (!st) return false;
-  for (int i = 0; i < 3; ++i)
-    if (st[i] <= 0 || st[i] % 8 != 0) return false;
-  return true;
-}
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-size_t ws_acc_bytes(int64_t rows, int64_t splits, int D) {
-  const size_t b = static_cast<size_t>(rows) * splits * D * sizeof(float);
-  return (b + 255) & ~static_cast<size_t>(255);
-}
-
-size_t ws_bytes(int batch, int seqlen_q, int Hq, int D, int max_seqlen_k) {
-  const int64_t rows = static_cast<int64_t>(batch) * seqlen_q * Hq;
-  const int64_t splits = max_seqlen_k > 0 ? ceil_div(max_seqlen_k, pkv::kSplitTokens) : 1;
-  return ws_acc_bytes(rows, splits, D) + static_cast<size_t>(rows) * splits * 2 * sizeof(float);
-}
+using namespace pkv;
 
 // TMA map over one cache view [num_blocks, block_size, Hkv, D] with the given
 // element strides (block, slot, head).  Dimension 0 is head_dim; the head and
@@ -230,26 +175,6 @@ int launch_bwd(const pkv::BwdParams &p, int64_t kv_ctas, int64_t q_ctas, const C
   kv<<<static_cast<unsigned>(kv_ctas), pkv::kBwdThreads, kKvSmem, s>>>(p, mk, mv, mq, mg);
   if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
   qk<<<static_cast<unsigned>(q_ctas), pkv::kBwdQThreads, kQSmem, s>>>(p, mk, mv, mq, mg);
-  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
-}
-
-// Few rows (decode: rows x splits partials spread over one block per row)
-// or many (prefill, packed batches: one warp per row).
-// Few rows (decode: rows x splits partials spread over one block per row)
-// or many (prefill, packed batches: one warp per row).
-template <int D>
-int launch_merge(const pkv::MergeParams &m, int64_t rows, cudaStream_t s) {
-  if (rows <= 4096) {
-    pkv::merge_kernel<D, true><<<static_cast<unsigned>(rows), D, 0, s>>>(m);
-    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
-  }
-  // the warps stride over the rows: at most 8 blocks of 8 warps per SM
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
-  const int64_t need = ceil_div(rows, pkv::kMergeRowsPerBlock);
-  const int64_t cap = static_cast<int64_t>(sm_count(dev)) * 8;
-  const int64_t blocks = need < cap ? need : cap;
-  pkv::merge_kernel<D, false><<<static_cast<unsigned>(blocks), 32 * pkv::kMergeRowsPerBlock, 0, s>>>(m);
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
