@@ -15,8 +15,8 @@
 //   m     the row's running reference (-inf at the split's start) rises to
 //           max(w) - kRefDrop when max(w) > m + 8; P = 2^(w - m) is then at
 //           most 2^8 and at least 2^(8 - kRefSlack) for the largest token;
-//   O^T  += V8^T * [P_hi + P_mid + P_lo]^T, P as three 8-bit operands of one
-//           scale (split_p: fp16's 11 bits);
+//   O^T  += V8^T * [P_hi | P_mid]^T, P as two 8-bit operands side by side
+//           (split_p), joined as O_hi + O_mid / 16 at the split's end;
 //   l     = sum of 2^(w - ev - m) = P 2^-ev over the tokens, in fp32.
 // (m, l, O) is a partial in the form the merge folds: out = O / l and lse =
 // (m + log2 l) ln 2.  Folding the V scale into the exponent keeps every
@@ -34,6 +34,9 @@
 #include "f8.cuh"
 
 namespace pkv {
+
+constexpr int kQ8Threads = 512;  // attn_split.cuh's roles, and
+constexpr int kPvWarp = 15;      // a second MMA issuer, for P.V
 
 // P <= 2^8 fits e4m3 (448); the reference moves when the largest token passes
 // it, and then to 2^kRefDrop below that token, so a row's largest P stays in
@@ -56,9 +59,10 @@ struct Q8Cfg {
   static constexpr int kAtom = 8 * D;                  // bytes of 8 rows, the swizzle's period
   static constexpr int kQPiece = N * D;                // q_hi, then q_lo
   static constexpr int kQBytes = 2 * kQPiece;
-  static constexpr int kPPiece = kTileTokens * N;      // P_hi, P_mid, P_lo
-  static constexpr int kPBytes = 3 * kPPiece;
-  static constexpr int kPKGroup = (N / 16) * 128;      // P^T stride between 8-token groups
+  static constexpr int kPCols = 2 * N;                 // P^T columns: N hi, then N mid
+  static constexpr int kPBytes = kTileTokens * kPCols;
+  static constexpr int kPKGroup = (kPCols / 16) * 128;  // P^T stride between 8-token groups
+  static constexpr int kSB = 4;                         // S^T buffers
   static constexpr int kOffK = 0;
   static constexpr int kOffV = NS * kKVBytes;
   static constexpr int kOffQ = 2 * NS * kKVBytes;
@@ -67,32 +71,37 @@ struct Q8Cfg {
   static constexpr int kSchedScratch = kOffSmall - kOffQ;  // bytes free at kernel start
   struct Small {
     uint64_t full_k[NS], empty_k[NS], full_v[NS], empty_v[NS];
-    uint64_t s_full[2], p_full[2], o_full[2], stat_free[2];
-    uint64_t m_full[2];     // [tile parity]: the tile's running references are published
+    uint64_t s_full[kSB], s_free[kSB], p_full[2], o_full[2], stat_free[2];
+    uint64_t m_full[2];     // [tile parity]: the tile's running references are published and
+                            // those of the tile before it read
     uint64_t unit_done[2];  // [O buffer]: a unit's last P.V completed
     uint64_t o_free[2];     // [O buffer]: the unit's O is read out
-    uint64_t q_full[kQB], q_empty[kQB], drain;
+    uint64_t q_full[kQB], q_empty[kQB], drain[2];
     uint32_t tmem_base;
     int abort_any;
     __align__(16) float wmax[2][2][4][N];  // [softmax warpgroup][tile parity][warp][row]
     __align__(16) float wsum[2][4][N];     // [buffer][warp][row]: per-warp sums
     float mnew[2][N];                      // [buffer][row]: the reference after the tile
+    __align__(16) float mw[2][4][N];       // [softmax warpgroup][warp][row]: the warp's copy of it
+    __align__(16) float aw[2][4][N];       // ... and of the factor
     float scl[2][N];                       // [buffer][row]: factor O and l take before it
     float mrun[2][N];                      // [tile parity][row]: mnew for the next tile
-    float rowf[kQB][N];                    // [Q buffer][row]: c 2^-k
+    __align__(16) float rowf[kQB][N];      // [Q buffer][row]: c 2^-k
     float fin_m[N], fin_l[N];              // each row's (m, l) for the direct final write
     int sched_list[kSchedMaxMine];
     int sched_meta[kSchedMaxMine][3];
     int sched_hist[kSchedHist], sched_start[kSchedBuckets];
     int sched_count;
-    int lim[2][N];                         // [softmax warpgroup][row]: key limit
+    __align__(16) int lim[2][N];           // [softmax warpgroup][row]: key limit
     int tab[2][2][kSplitTokens / 16];      // [producer][unit parity]: block-table entries
     uint8_t sctab[2][2][kSplitTokens / 16];  // [unit parity][K, V]: the entries' scale bytes
     uint8_t sc[NS][2][8];                  // [stage][K, V][box]: scale bytes of the stage's tile
   };
   static constexpr int kSmemBytes = kOffSmall + static_cast<int>(sizeof(Small)) + 1024;
-  // TMEM: S^T (N columns) x 2 buffers, then O^T (N columns) x 2 buffers
-  static constexpr int kTmemCols = (4 * N <= 64) ? 64 : 256;
+  // TMEM: S^T (N columns) x kSB buffers, then O^T (hi and mid, 2N columns) x 2
+  // buffers (alternate units)
+  static constexpr int kTmemCols = N == 16 ? 128 : 512;
+  static constexpr uint32_t kColO = kSB * N;
 };
 
 // A scale byte, held to the range that the arithmetic covers (a byte outside
@@ -105,20 +114,63 @@ __device__ __forceinline__ int checked_scale(int byte, int32_t *err) {
   return byte;
 }
 
-// The K and V scale bytes of the table entries of unit x's split.
-__device__ __forceinline__ void stage_scales(const Q8Params &p, const Unit &x, const int *tab,
-                                             uint8_t (*sctab)[kSplitTokens / 16], int lane) {
+// A unit's block-table entries and their scale bytes on the way to shared
+// memory, a lane's share in registers: the loads of the next unit go out
+// before the tiles of this one are issued and are used after them.  (Under a
+// saturated memory system a load takes microseconds, and at a unit's boundary
+// every tile behind it waits: loading there cost 10 us per unit.)
+constexpr int kTabBatch = kSplitTokens / 16 / 32;  // entries per lane at most
+
+struct TabRegs {
+  int blk[kTabBatch], kb[kTabBatch], vb[kTabBatch];
+};
+
+__device__ __forceinline__ int tab_entries(const Q8Params &p, const Unit &x) {
   const int ntok = min(kSplitTokens, x.lim_max - x.tok0);
-  const int nent = (ntok + (1 << p.block_shift) - 1) >> p.block_shift;
-  for (int e = lane; e < nent; e += 32) {
-    const int blk = tab[e];
-    int kb = 127, vb = 127;
-    if (blk >= 0 && static_cast<int64_t>(blk) < p.num_blocks) {  // (kPastWidth is negative)
-      kb = checked_scale(__ldg(p.k_sc + blk * p.ksc_sb + x.kvh * p.ksc_sh), p.err);
-      vb = checked_scale(__ldg(p.v_sc + blk * p.vsc_sb + x.kvh * p.vsc_sh), p.err);
+  return (ntok + (1 << p.block_shift) - 1) >> p.block_shift;
+}
+
+__device__ __forceinline__ void load_tab(const Q8Params &p, const Unit &x, TabRegs &r, int lane) {
+  const int nent = tab_entries(p, x), first = x.tok0 >> p.block_shift;
+#pragma unroll
+  for (int i = 0; i < kTabBatch; ++i) {
+    const int e = lane + 32 * i;
+    r.blk[i] = kPastWidth;
+    if (e < nent && first + e < p.max_blocks_per_seq)
+      r.blk[i] = __ldg(p.block_table + x.b * p.bt_stride + first + e);
+  }
+}
+
+__device__ __forceinline__ void load_scales(const Q8Params &p, const Unit &x, TabRegs &r) {
+#pragma unroll
+  for (int i = 0; i < kTabBatch; ++i) {
+    const int64_t blk = r.blk[i];
+    r.kb[i] = r.vb[i] = 127;
+    if (blk >= 0 && blk < p.num_blocks) {  // (kPastWidth is negative)
+      r.kb[i] = __ldg(p.k_sc + blk * p.ksc_sb + x.kvh * p.ksc_sh);
+      r.vb[i] = __ldg(p.v_sc + blk * p.vsc_sb + x.kvh * p.vsc_sh);
     }
-    sctab[0][e] = static_cast<uint8_t>(kb);
-    sctab[1][e] = static_cast<uint8_t>(vb);
+  }
+}
+
+__device__ __forceinline__ void put_tab(const Q8Params &p, const Unit &x, const TabRegs &r, int *tab,
+                                        int lane) {
+  const int nent = tab_entries(p, x);
+#pragma unroll
+  for (int i = 0; i < kTabBatch; ++i)
+    if (lane + 32 * i < nent) tab[lane + 32 * i] = r.blk[i];
+}
+
+__device__ __forceinline__ void put_scales(const Q8Params &p, const Unit &x, const TabRegs &r,
+                                           uint8_t (*sctab)[kSplitTokens / 16], int lane) {
+  const int nent = tab_entries(p, x);
+#pragma unroll
+  for (int i = 0; i < kTabBatch; ++i) {
+    const int e = lane + 32 * i;
+    if (e < nent) {
+      sctab[0][e] = static_cast<uint8_t>(checked_scale(r.kb[i], p.err));
+      sctab[1][e] = static_cast<uint8_t>(checked_scale(r.vb[i], p.err));
+    }
   }
 }
 
@@ -129,54 +181,54 @@ __device__ __forceinline__ int swz16(int r, int c) {
   return r * D + ((D == 128 ? (c ^ (r & 7)) : (c ^ ((r >> 1) & 3))) << 4);
 }
 
-// Stage the query rows of unit x as q_hi and q_lo (the B operands of S^T) and
-// their factors c 2^-k; padded rows are zero.  D / 8 lanes share a row, eight
-// elements each.
+// The query rows of unit x as q_hi and q_lo (the B operands of S^T) and their
+// factors c 2^-k.  D / 8 lanes share a row, eight elements each; a pass of the
+// warp takes 256 / D rows.  Rows past x.rows keep whatever the buffer holds:
+// their columns of S^T are never used.
+template <int D>
+__device__ __forceinline__ uint4 load_q_pass(const Q8Params &p, const Unit &x, int pass, int lane) {
+  constexpr int kLanes = D / 8;
+  const int c = pass * (32 / kLanes) + lane / kLanes;
+  if (c >= x.rows) return make_uint4(0u, 0u, 0u, 0u);
+  const int r = x.row0 + c;
+  const int i = r / p.G, g = r - i * p.G;
+  return __ldg(reinterpret_cast<const uint4 *>(p.q + q_tok_off(p, x, i) +
+                                               static_cast<int64_t>(x.kvh * p.G + g) * p.q_sh) +
+               lane % kLanes);
+}
+
 template <int D, int N>
-__device__ __forceinline__ void stage_q8(const Q8Params &p, const Unit &x, uint8_t *qdst,
-                                         float *rowf, int lane) {
-  constexpr int kLanes = D / 8, kRowsPerPass = 32 / kLanes;
-  const int ch = lane % kLanes;
-#pragma unroll 4
-  for (int c0 = 0; c0 < N; c0 += kRowsPerPass) {
-    const int c = c0 + lane / kLanes;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (c < x.rows) {
-      const int r = x.row0 + c;
-      const int i = r / p.G, g = r - i * p.G;
-      v = __ldg(reinterpret_cast<const uint4 *>(p.q + q_tok_off(p, x, i) +
-                                                static_cast<int64_t>(x.kvh * p.G + g) * p.q_sh +
-                                                ch * 8));
-    }
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t top = 0;  // largest magnitude as bits: ordered like the values, NaN and inf on top
+__device__ __forceinline__ void put_q_pass(const Q8Params &p, uint4 v, int pass, uint8_t *qdst,
+                                           float *rowf, int lane) {
+  constexpr int kLanes = D / 8;
+  const int ch = lane % kLanes, c = pass * (32 / kLanes) + lane / kLanes;
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t top = 0;  // largest magnitude as bits: ordered like the values, NaN and inf on top
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
+  for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
 #pragma unroll
-    for (int off = kLanes / 2; off >= 1; off >>= 1)
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-    const bool finite = top < 0x7F80u;
-    // largest magnitude to [128, 256): exponent field + k = 127 + 7; held to
-    // [-60, 60] so that c 2^-k 2^ek stays a normal number (rows below 2^-53
-    // keep fewer bits, values past 2^68 saturate)
-    int k = 134 - max(static_cast<int>(top >> 7), 1);
-    k = !finite || top == 0 ? 0 : max(-60, min(60, k));
-    // a row with an infinity or NaN: those elements become NaN, the rest zero
-    const float f = finite ? __int_as_float((127 + k) << 23) : 0.f;
-    uint32_t hi[2], lo[2];
+  for (int off = kLanes / 2; off >= 1; off >>= 1)
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+  const bool finite = top < 0x7F80u;
+  // largest magnitude to [128, 256): exponent field + k = 127 + 7; held to
+  // [-60, 60] so that c 2^-k 2^ek stays a normal number (rows below 2^-53
+  // keep fewer bits, values past 2^68 saturate)
+  int k = 134 - max(static_cast<int>(top >> 7), 1);
+  k = !finite || top == 0 ? 0 : max(-60, min(60, k));
+  // a row with an infinity or NaN: those elements become NaN, the rest zero
+  const float f = finite ? __int_as_float((127 + k) << 23) : 0.f;
+  uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const Split2 s = split_q(__fmul_rn(__uint_as_float(w[e] << 16), f),
-                               __fmul_rn(__uint_as_float(w[e] & 0xFFFF0000u), f));
-      hi[e >> 1] = (e & 1) ? hi[e >> 1] | (s.hi << 16) : s.hi;
-      lo[e >> 1] = (e & 1) ? lo[e >> 1] | (s.lo << 16) : s.lo;
-    }
-    uint8_t *dst = qdst + swz16<D>(c, ch >> 1) + (ch & 1) * 8;
-    *reinterpret_cast<uint2 *>(dst) = make_uint2(hi[0], hi[1]);
-    *reinterpret_cast<uint2 *>(dst + N * D) = make_uint2(lo[0], lo[1]);
-    if (ch == 0) rowf[c] = __fmul_rn(p.cscale, __int_as_float((127 - k) << 23));
+  for (int e = 0; e < 4; ++e) {
+    const Split2 s = split_q(__fmul_rn(__uint_as_float(w[e] << 16), f),
+                             __fmul_rn(__uint_as_float(w[e] & 0xFFFF0000u), f));
+    hi[e] = s.hi;
+    lo[e] = s.lo;
   }
+  uint8_t *dst = qdst + swz16<D>(c, ch >> 1) + (ch & 1) * 8;
+  *reinterpret_cast<uint2 *>(dst) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+  *reinterpret_cast<uint2 *>(dst + N * D) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+  if (ch == 0) rowf[c] = __fmul_rn(p.cscale, __int_as_float((127 - k) << 23));
 }
 
 // One producer warp (K and the query rows, or V and the scales); the stage
@@ -198,27 +250,54 @@ __device__ __forceinline__ void produce_q8(const Q8Params &p, const CUtensorMap 
   if (cu >= 0) {
     const int bmask = (1 << p.block_shift) - 1;
     int ui = 0, gi = 0;
-    auto stage = [&](const Unit &u, int ord) {
-      stage_tab(p, u, tabs[ord & 1], lane);
-      if (!is_k) {
-        __syncwarp();
-        stage_scales(p, u, tabs[ord & 1], sm->sctab[ord & 1], lane);
+    constexpr int kPasses = N * D / 256;
+    constexpr bool kEarly = kPasses <= 8;  // the next unit's Q waits in registers too
+    TabRegs tr;
+    uint4 qr[kEarly ? kPasses : 1];
+    auto load_q = [&](const Unit &u) {
+      if constexpr (kEarly) {
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i)
+          if (i * (256 / D) < u.rows) qr[i] = load_q_pass<D>(p, u, i, lane);
       }
     };
     auto put_q = [&](const Unit &u, int ord) {
-      stage_q8<D, N>(p, u, smem + C::kOffQ + (ord % QB) * C::kQBytes, sm->rowf[ord % QB], lane);
+      uint8_t *dst = smem + C::kOffQ + (ord % QB) * C::kQBytes;
+      float *rowf = sm->rowf[ord % QB];
+      if constexpr (kEarly) {
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i)
+          if (i * (256 / D) < u.rows) put_q_pass<D, N>(p, qr[i], i, dst, rowf, lane);
+      } else {
+#pragma unroll 4
+        for (int i = 0; i < kPasses; ++i)
+          if (i * (256 / D) < u.rows)
+            put_q_pass<D, N>(p, load_q_pass<D>(p, u, i, lane), i, dst, rowf, lane);
+      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm->q_full[ord % QB]);
     };
-    stage(cur, 0);
+    load_tab(p, cur, tr, lane);
+    if (is_k) load_q(cur);
+    put_tab(p, cur, tr, tabs[0], lane);
+    if (is_k) {
+      put_q(cur, 0);
+    } else {
+      load_scales(p, cur, tr);
+      put_scales(p, cur, tr, sm->sctab[0], lane);
+    }
     __syncwarp();
-    if (is_k) put_q(cur, 0);
     while (true) {
-      // stage the next unit while this one's tiles are issued
       Unit nxt;
       const int nu = next_unit<N>(p, sc, cu + 1, nxt);
-      if (nu >= 0) stage(nxt, ui + 1);
+      if (nu >= 0) {
+        load_tab(p, nxt, tr, lane);
+        if (is_k) load_q(nxt);
+      }
+      // V: the entries have arrived a few tiles on, and their scales are
+      // fetched behind the remaining ones
+      const int j_scales = min(cur.n_tiles - 1, 4);
       const int *tab = tabs[ui & 1];
       for (int j = 0; j < cur.n_tiles && !failed; ++j, ++gi) {
         const int st = gi % NS;
@@ -259,8 +338,12 @@ __device__ __forceinline__ void produce_q8(const Q8Params &p, const CUtensorMap 
           last_gi[st] = gi;
         }
         if (errs && p.err) atomicOr(p.err, errs);
+        if (!is_k && nu >= 0 && j == j_scales) load_scales(p, nxt, tr);
       }
       if (failed || nu < 0) break;
+      // (the other parity's entries were last read for the unit before this one)
+      put_tab(p, nxt, tr, tabs[(ui + 1) & 1], lane);
+      if (!is_k) put_scales(p, nxt, tr, sm->sctab[(ui + 1) & 1], lane);
       // The next unit's Q goes into the buffer of the unit before this one,
       // once its last QK^T and its epilogue (staged there) are done; see
       // produce() for why the wait comes after this unit's last tile.
@@ -290,7 +373,7 @@ __device__ __forceinline__ void produce_q8(const Q8Params &p, const CUtensorMap 
 }
 
 template <int D, int N, int NS>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kQ8Threads, 1)
     attn_split_q8_kernel(const __grid_constant__ Q8Params p,
                          const __grid_constant__ CUtensorMap map_k,
                          const __grid_constant__ CUtensorMap map_v) {
@@ -311,18 +394,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm->full_v[i], 1);
       mbar_init(&sm->empty_v[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::kSB; ++i) {
       mbar_init(&sm->s_full[i], 1);
+      mbar_init(&sm->s_free[i], 4);   // one arrival per warp of a softmax warpgroup
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&sm->p_full[i], 4);   // one arrival per warp of a softmax warpgroup
       mbar_init(&sm->o_full[i], 1);
       mbar_init(&sm->stat_free[i], 4);
-      mbar_init(&sm->m_full[i], 1);
+      mbar_init(&sm->m_full[i], 4);   // one arrival per warp of a softmax warpgroup
       mbar_init(&sm->unit_done[i], 1);
       mbar_init(&sm->o_free[i], 4);   // one arrival per correction warp
       mbar_init(&sm->q_full[i], 1);
       mbar_init(&sm->q_empty[i], 2);  // the unit's last QK^T, and its epilogue
+      mbar_init(&sm->drain[i], 1);
     }
-    mbar_init(&sm->drain, 1);
     sm->abort_any = 0;
     fence_barrier_init();
   }
@@ -337,7 +423,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (p.sched) {
     build_schedule<N>(p, smem + C::kOffQ, C::kSchedScratch, sm->sched_hist, sm->sched_start,
                       sm->sched_list, sm->sched_meta, &sm->sched_count);
-    if (sm->sched_count >= 0) sc = Sched{sm->sched_list, sm->sched_meta, sm->sched_count};
+    if (sm->sched_count >= 0) {
+      sc = Sched{sm->sched_list, sm->sched_meta, sm->sched_count};
+    } else if (sc.count <= kSchedMaxMine) {
+      // nothing to balance: the stride-grid deal as a list, so that no role
+      // reads global memory between units
+      for (int k = threadIdx.x; k < sc.count; k += kQ8Threads) {
+        const int u = sc.unit(k), b = unit_seq(p, u);
+        sm->sched_list[k] = u;
+        sm->sched_meta[k][0] = __ldg(p.seqlens + b);
+        sm->sched_meta[k][1] = p.cu_q ? __ldg(p.cu_q + b) : 0;
+        sm->sched_meta[k][2] = p.cu_q ? __ldg(p.cu_q + b + 1) : 0;
+      }
+      __syncthreads();
+      sc = Sched{sm->sched_list, sm->sched_meta, sc.count};
+    }
   }
 
   if (warp == kKWarp) {
@@ -346,94 +446,90 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kVWarp) {
     produce_q8<C>(p, &map_v, smem, sm, sm->full_v, sm->empty_v, sm->tab[1], C::kOffV, false, lane,
                   abort_any, sc);
-  } else if (warp == kMmaWarp) {
+  } else if (warp == kMmaWarp || warp == kPvWarp) {
     // ------------------------------------------------------------------
-    // MMA issuer (one thread): QK^T of tile gi, then P.V of tile gi - 1
+    // MMA issuers, one thread each: QK^T of every tile as soon as its K and a
+    // S^T buffer are there, and P.V of every tile as soon as its P and V are.
+    // One thread for both spent 1750 cycles on a tile (issue of 12 small MMAs
+    // and 5 commits, and the waits between), more than the 1500 that the
+    // tile's 32 KB take from memory.
     // ------------------------------------------------------------------
     if (lane == 0) {
+      const bool is_qk = warp == kMmaWarp;
       // A = K tile, B = q_hi / q_lo (K-major); A = V^T, B = P^T (MN-major)
       constexpr uint32_t kQkHi = idesc_f8(128, N, kFmtE4M3, kFmtE4M3, 0, 0);
       constexpr uint32_t kQkLo = idesc_f8(128, N, kFmtE4M3, kFmtE5M2, 0, 0);
-      constexpr uint32_t kPvHi = idesc_f8(128, N, kFmtE4M3, kFmtE4M3, 1, 1);
-      constexpr uint32_t kPvLo = idesc_f8(128, N, kFmtE4M3, kFmtE5M2, 1, 1);
-      const uint32_t tS = tmem, tO = tmem + 2 * N;
-      struct Pend {
-        int g, first, last, u;
-      };
+      constexpr uint32_t kPv = idesc_f8(128, C::kPCols, kFmtE4M3, kFmtE4M3, 1, 1);
       int gi = 0, ui = 0;
-      Pend prev{-1, 0, 0, 0};
       bool failed = false;
-      auto pv_step = [&](const Pend &pd) -> bool {
-        const int g = pd.g, st = g % NS, bb = g & 1, ob = pd.u & 1;
-        if (!mbar_wait(&sm->p_full[bb], (g >> 1) & 1, abort_any, p.wait_ns)) return false;
-        if (pd.first && !mbar_wait(&sm->o_free[ob], ((pd.u >> 1) & 1) ^ 1, abort_any, p.wait_ns))
-          return false;
-        if (!mbar_wait(&sm->full_v[st], (g / NS) & 1, abort_any, p.wait_ns)) return false;
-        tc_fence_after_sync();
-        const uint32_t vaddr = sbase + C::kOffV + st * C::kKVBytes;
-        const uint32_t paddr = sbase + C::kOffP + bb * C::kPBytes;
-#pragma unroll
-        for (int kk = 0; kk < kTileTokens / 32; ++kk) {
-          // V^T: MN-major, 32 tokens (four 8-token atoms) per step.  D = 64:
-          // both M halves read the same 64 columns; lanes 64..127 are unused.
-          const uint64_t a = smem_desc(vaddr + kk * 4 * C::kAtom, 0, C::kAtom, C::kLayout);
-          // P^T: MN-major, no swizzle; 16-column groups 128 B apart, 8-token
-          // groups kPKGroup apart
-#pragma unroll
-          for (int piece = 0; piece < 3; ++piece) {
-            const uint64_t b = smem_desc(paddr + piece * C::kPPiece + kk * 4 * C::kPKGroup,
-                                         C::kPKGroup, 128, kLayoutInterleave);
-            umma_f8(tO + ob * N, a, b, piece == 0 ? kPvHi : kPvLo,
-                    (pd.first && kk == 0 && piece == 0) ? 0u : 1u);
-          }
-        }
-        umma_commit(&sm->o_full[bb]);
-        if (pd.last) umma_commit(&sm->unit_done[ob]);
-        umma_commit(&sm->empty_v[st]);
-        return true;
-      };
       for (int k = 0; k < sc.count && !failed; ++k) {
         const Unit x = sc.get<N>(p, k);
         if (x.n_tiles == 0) continue;
-        const int qb = ui % QB;
-        if (!mbar_wait(&sm->q_full[qb], (ui / QB) & 1, abort_any, p.wait_ns)) {
-          failed = true;
-          break;
-        }
-        const uint32_t qaddr = sbase + C::kOffQ + qb * C::kQBytes;
-        for (int j = 0; j < x.n_tiles; ++j, ++gi) {
-          const int st = gi % NS, bb = gi & 1;
-          if (!mbar_wait(&sm->full_k[st], (gi / NS) & 1, abort_any, p.wait_ns)) {
+        if (is_qk) {
+          const int qb = ui % QB;
+          if (!mbar_wait(&sm->q_full[qb], (ui / QB) & 1, abort_any, p.wait_ns)) {
             failed = true;
             break;
           }
-          tc_fence_after_sync();
-          const uint32_t kaddr = sbase + C::kOffK + st * C::kKVBytes;
+          const uint64_t bh = smem_desc(sbase + C::kOffQ + qb * C::kQBytes, 16, C::kAtom, C::kLayout);
+          for (int j = 0; j < x.n_tiles; ++j, ++gi) {
+            const int st = gi % NS, sb = gi % C::kSB;
+            if (!mbar_wait(&sm->full_k[st], (gi / NS) & 1, abort_any, p.wait_ns) ||
+                !mbar_wait(&sm->s_free[sb], ((gi / C::kSB) & 1) ^ 1, abort_any, p.wait_ns)) {
+              failed = true;
+              break;
+            }
+            tc_fence_after_sync();
+            const uint64_t a = smem_desc(sbase + C::kOffK + st * C::kKVBytes, 16, C::kAtom, C::kLayout);
+            const uint32_t d = tmem + sb * N;
 #pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk) {
-            const uint64_t a = smem_desc(kaddr + kk * 32, 16, C::kAtom, C::kLayout);
-            const uint64_t bh = smem_desc(qaddr + kk * 32, 16, C::kAtom, C::kLayout);
-            const uint64_t bl = smem_desc(qaddr + C::kQPiece + kk * 32, 16, C::kAtom, C::kLayout);
-            umma_f8(tS + bb * N, a, bh, kQkHi, kk > 0 ? 1u : 0u);
-            umma_f8(tS + bb * N, a, bl, kQkLo, 1u);
+            for (int kk = 0; kk < D / 32; ++kk) {
+              umma_f8(d, a + kk * 2, bh + kk * 2, kQkHi, kk > 0 ? 1u : 0u);
+              umma_f8(d, a + kk * 2, bh + (C::kQPiece >> 4) + kk * 2, kQkLo, 1u);
+            }
+            umma_commit(&sm->s_full[sb]);
+            umma_commit(&sm->empty_k[st]);
+            if (j == x.n_tiles - 1) umma_commit(&sm->q_empty[qb]);
           }
-          umma_commit(&sm->s_full[bb]);
-          umma_commit(&sm->empty_k[st]);
-          if (j == x.n_tiles - 1) umma_commit(&sm->q_empty[qb]);
-          if (prev.g >= 0 && !pv_step(prev)) {
+        } else {
+          const int ob = ui & 1;
+          const uint32_t d = tmem + C::kColO + ob * C::kPCols;
+          if (!mbar_wait(&sm->o_free[ob], ((ui >> 1) & 1) ^ 1, abort_any, p.wait_ns)) {
             failed = true;
             break;
           }
-          prev = Pend{gi, j == 0 ? 1 : 0, j == x.n_tiles - 1 ? 1 : 0, ui};
+          for (int j = 0; j < x.n_tiles; ++j, ++gi) {
+            const int st = gi % NS, bb = gi & 1;
+            if (!mbar_wait(&sm->full_v[st], (gi / NS) & 1, abort_any, p.wait_ns) ||
+                !mbar_wait(&sm->p_full[bb], (gi >> 1) & 1, abort_any, p.wait_ns)) {
+              failed = true;
+              break;
+            }
+            tc_fence_after_sync();
+            // V^T: MN-major, 32 tokens (four 8-token atoms) per step.  D = 64:
+            // both M halves read the same 64 columns; lanes 64..127 are unused.
+            const uint64_t a = smem_desc(sbase + C::kOffV + st * C::kKVBytes, 0, C::kAtom, C::kLayout);
+            // P^T: MN-major, no swizzle; 16-column groups 128 B apart, 8-token
+            // groups kPKGroup apart
+            const uint64_t b = smem_desc(sbase + C::kOffP + bb * C::kPBytes, C::kPKGroup, 128,
+                                         kLayoutInterleave);
+#pragma unroll
+            for (int kk = 0; kk < kTileTokens / 32; ++kk)
+              umma_f8(d, a + kk * (4 * C::kAtom >> 4), b + kk * (4 * C::kPKGroup >> 4), kPv,
+                      (j == 0 && kk == 0) ? 0u : 1u);
+            umma_commit(&sm->o_full[bb]);
+            umma_commit(&sm->empty_v[st]);
+            if (j == x.n_tiles - 1) umma_commit(&sm->unit_done[ob]);
+          }
         }
         ++ui;
       }
-      if (!failed && prev.g >= 0) failed = !pv_step(prev);
       // every MMA this thread issued completes before TMEM is released
       (void)failed;
-      umma_commit(&sm->drain);
+      uint64_t *drain = &sm->drain[is_qk ? 0 : 1];
+      umma_commit(drain);
       volatile int no_abort = 0;
-      mbar_wait(&sm->drain, 0, &no_abort);
+      mbar_wait(drain, 0, &no_abort);
     }
   } else if (warp < kCorrWarp0) {
     // ------------------------------------------------------------------
@@ -449,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; k < sc.count && !stop; ++k) {
       const Unit x = sc.get<N>(p, k);
       if (x.n_tiles == 0) continue;
-      const uint32_t ocol = tmem + lane_off + 2 * N + (uo & 1) * N;  // this unit's O^T
+      const uint32_t ocol = tmem + lane_off + C::kColO + (uo & 1) * C::kPCols;  // this unit's O^T
       if (t < N) {
         int lim = 0;
         if (t < x.rows) {
@@ -471,11 +567,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < x.n_tiles; ++j) {
         const int gi = gbase + j;
         if ((gi & 1) != wg) continue;
-        const int bb = wg, st = gi % NS, par = (gi >> 1) & 1;
+        const int bb = wg, st = gi % NS, sb = gi % C::kSB, par = (gi >> 1) & 1;
         // V landed: the stage's scale bytes are staged with it (the stage is
         // not refilled before this tile's P.V)
         bool ok = mbar_wait(&sm->full_v[st], (gi / NS) & 1, abort_any, p.wait_ns);
-        ok = mbar_wait(&sm->s_full[bb], par, abort_any, p.wait_ns) && ok;
+        ok = mbar_wait(&sm->s_full[sb], (gi / C::kSB) & 1, abort_any, p.wait_ns) && ok;
         // P^T[bb] is free once P.V of tile gi - 2 is done, the row statistics
         // once the correction of tile gi - 2 has read them
         ok = mbar_wait(&sm->o_full[bb], par ^ 1, abort_any, p.wait_ns) && ok;
@@ -485,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int ch = 0; ch < N / 16; ++ch)
           if (ch * 16 < x.rows)
-            tmem_ld16(tmem + lane_off + bb * N + ch * 16, *reinterpret_cast<float(*)[16]>(&sv[ch * 16]));
+            tmem_ld16(tmem + lane_off + sb * N + ch * 16, *reinterpret_cast<float(*)[16]>(&sv[ch * 16]));
         const int tok0 = x.tok0 + j * kTileTokens;
         const int tok = tok0 + t;
         const bool held = tok < x.lim_max;
@@ -495,6 +591,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int ch = 0; ch < N / 16; ++ch)
           if (ch * 16 < x.rows) tmem_ld_wait_for(*reinterpret_cast<float(*)[16]>(&sv[ch * 16]));
+        // the S^T buffer is read
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm->s_free[sb]);
         if (tok0 + kTileTokens > x.lim_max && ok && !held) {
           // The last tile: keys past the loaded range hold stale bytes; zero
           // those V rows so that 0 * V stays 0 in P.V.
@@ -506,16 +606,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int q4 = 0; q4 < N / 4; ++q4) {
           if (q4 * 4 < x.rows) {  // warp-uniform: padded rows need no reduction
+            const int4 lim = *reinterpret_cast<const int4 *>(&sm->lim[wg][4 * q4]);
+            const float4 rf = *reinterpret_cast<const float4 *>(&rowf[4 * q4]);
+            const int lims[4] = {lim.x, lim.y, lim.z, lim.w};
+            const float rfs[4] = {rf.x, rf.y, rf.z, rf.w};
             float v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int c = 4 * q4 + e;
-              // (masked: the score itself is -inf from here on)
-              sv[c] = (c < x.rows && tok < sm->lim[wg][c]) ? sv[c] : NEG_INF;
-              v[e] = __fmaf_rn(sv[c], __fmul_rn(rowf[c], ks), ev);
-              if (sv[c] == NEG_INF) v[e] = NEG_INF;
+              // (masked, and rows past x.rows, whose limit is 0: the score
+              // itself is -inf from here on)
+              const bool seen = tok < lims[e];
+              sv[c] = seen ? sv[c] : NEG_INF;
+              v[e] = seen ? __fmaf_rn(sv[c], __fmul_rn(rfs[e], ks), ev) : NEG_INF;
             }
-            warp_max4(v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = warp_max(v[e]);
             if (lane == 0)
               *reinterpret_cast<float4 *>(&wmax[wq][4 * q4]) = make_float4(v[0], v[1], v[2], v[3]);
           }
@@ -524,28 +630,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           stop = true;
           break;
         }
-        // the running references: the previous tile's, this tile's
+        // the running references: the previous tile's, this tile's.  Every
+        // warp works them out for itself (lane = row), so that the chain from
+        // tile to tile has no barrier in it; warp 0 publishes them.
         if (gi > 0)
           ok = mbar_wait(&sm->m_full[(gi - 1) & 1], ((gi - 1) >> 1) & 1, abort_any, p.wait_ns) && ok;
-        if (t < N) {
-          float m_new = NEG_INF, a = 1.f;
-          if (t < x.rows) {
-            const float tmax = fmaxf(fmaxf(wmax[0][t], wmax[1][t]), fmaxf(wmax[2][t], wmax[3][t]));
-            const float m_prev = j > 0 ? sm->mrun[(gi - 1) & 1][t] : NEG_INF;
-            m_new = (tmax > __fadd_rn(m_prev, kRefTop)) ? __fsub_rn(tmax, kRefDrop) : m_prev;
-            a = (m_prev == NEG_INF || m_new == m_prev) ? 1.f : ex2(__fsub_rn(m_prev, m_new));
+        bool moved = false;
+#pragma unroll
+        for (int c0 = 0; c0 < N; c0 += 32) {
+          const int c = c0 + lane;
+          if (c < N) {
+            float m_new = NEG_INF, a = 1.f;
+            if (c < x.rows) {
+              const float tmax = fmaxf(fmaxf(wmax[0][c], wmax[1][c]), fmaxf(wmax[2][c], wmax[3][c]));
+              const float m_prev = j > 0 ? sm->mrun[(gi - 1) & 1][c] : NEG_INF;
+              m_new = (tmax > __fadd_rn(m_prev, kRefTop)) ? __fsub_rn(tmax, kRefDrop) : m_prev;
+              a = (m_prev == NEG_INF || m_new == m_prev) ? 1.f : ex2(__fsub_rn(m_prev, m_new));
+            }
+            sm->mw[wg][wq][c] = m_new;
+            sm->aw[wg][wq][c] = a;
+            moved = moved || a != 1.f;
+            if (wq == 0) {
+              sm->mrun[gi & 1][c] = m_new;
+              sm->mnew[bb][c] = m_new;
+              sm->scl[bb][c] = a;
+            }
           }
-          sm->mnew[bb][t] = m_new;
-          sm->scl[bb][t] = a;
-          sm->mrun[gi & 1][t] = m_new;
         }
-        if (wg_bar_or(bar_id, !ok)) {
-          stop = true;
-          break;
-        }
-        if (t == 0) mbar_arrive(&sm->m_full[gi & 1]);
-        bool resc = false;
-        for (int c = 0; c < x.rows; ++c) resc = resc || sm->scl[bb][c] != 1.f;
+        const bool resc = __any_sync(0xffffffffu, moved);  // (also orders mw / aw for the warp)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm->m_full[gi & 1]);
         if (resc) {
           // O^T holds the unit's tiles < gi once P.V(gi - 1) is done (see
           // attn_split.cuh on the parity)
@@ -555,46 +669,51 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int ch = 0; ch < N / 16; ++ch) {
               if (ch * 16 < x.rows) {  // warp-uniform
-                float o[16];
-                tmem_ld16(ocol + ch * 16, o);
-                tmem_ld_wait_for(o);
-                uint32_t w[16];
+                float hi[16], mid[16];
+                tmem_ld16(ocol + ch * 16, hi);
+                tmem_ld16(ocol + N + ch * 16, mid);
+                tmem_ld_wait_for(hi);
+                tmem_ld_wait_for(mid);
+                uint32_t wh[16], wm[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                  w[e] = __float_as_uint(__fmul_rn(o[e], sm->scl[bb][ch * 16 + e]));
-                tmem_st16(ocol + ch * 16, w);
+                for (int e = 0; e < 16; ++e) {
+                  const float a = sm->aw[wg][wq][ch * 16 + e];
+                  wh[e] = __float_as_uint(__fmul_rn(hi[e], a));
+                  wm[e] = __float_as_uint(__fmul_rn(mid[e], a));
+                }
+                tmem_st16(ocol + ch * 16, wh);
+                tmem_st16(ocol + N + ch * 16, wm);
               }
             }
             tmem_st_wait();
           }
         }
-        // P^T row t: one 16-byte chunk of each piece per 16 rows
+        // P^T row t: one 16-byte chunk of hi and of mid per 16 rows
         uint8_t *prow = smem + C::kOffP + bb * C::kPBytes + (t >> 3) * C::kPKGroup + (t & 7) * 16;
 #pragma unroll
         for (int grp = 0; grp < N / 16; ++grp) {
-          uint32_t w[3][4];
+          uint32_t wh[4], wm[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            Split3 a{0u, 0u, 0u}, b{0u, 0u, 0u};
-            if (grp * 16 + 4 * e < x.rows) {  // groups of padded rows keep p = 0
+            const int c0 = grp * 16 + 4 * e;
+            SplitP a{0u, 0u}, b{0u, 0u};
+            if (c0 < x.rows) {  // groups of padded rows keep p = 0
+              const float4 rf = *reinterpret_cast<const float4 *>(&rowf[c0]);
+              const float4 mm = *reinterpret_cast<const float4 *>(&sm->mw[wg][wq][c0]);
+              const float rfs[4] = {rf.x, rf.y, rf.z, rf.w}, ms[4] = {mm.x, mm.y, mm.z, mm.w};
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int c = grp * 16 + 4 * e + i;
-                sv[c] = (sv[c] == NEG_INF)
-                            ? 0.f
-                            : ex2(__fmaf_rn(sv[c], __fmul_rn(rowf[c], ks), __fsub_rn(ev, sm->mnew[bb][c])));
-              }
-              a = split_p(sv[grp * 16 + 4 * e], sv[grp * 16 + 4 * e + 1]);
-              b = split_p(sv[grp * 16 + 4 * e + 2], sv[grp * 16 + 4 * e + 3]);
+              for (int i = 0; i < 4; ++i)
+                sv[c0 + i] = (sv[c0 + i] == NEG_INF)
+                                 ? 0.f
+                                 : ex2(__fmaf_rn(sv[c0 + i], __fmul_rn(rfs[i], ks), __fsub_rn(ev, ms[i])));
+              a = split_p(sv[c0], sv[c0 + 1]);
+              b = split_p(sv[c0 + 2], sv[c0 + 3]);
             }
-            w[0][e] = a.hi | (b.hi << 16);
-            w[1][e] = a.mid | (b.mid << 16);
-            w[2][e] = a.lo | (b.lo << 16);
+            wh[e] = a.hi | (b.hi << 16);
+            wm[e] = a.mid | (b.mid << 16);
           }
-#pragma unroll
-          for (int piece = 0; piece < 3; ++piece)
-            *reinterpret_cast<uint4 *>(prow + piece * C::kPPiece + grp * 128) =
-                make_uint4(w[piece][0], w[piece][1], w[piece][2], w[piece][3]);
+          *reinterpret_cast<uint4 *>(prow + grp * 128) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
+          *reinterpret_cast<uint4 *>(prow + (N / 16 + grp) * 128) = make_uint4(wm[0], wm[1], wm[2], wm[3]);
         }
 #pragma unroll
         for (int q4 = 0; q4 < N / 4; ++q4) {
@@ -675,11 +794,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int ch = 0; ch < N / 16; ++ch) {
           if (ch * 16 < x.rows) {  // warp-uniform
-            float o[16];
-            tmem_ld16(tmem + lane_off + 2 * N + ob * N + ch * 16, o);
-            tmem_ld_wait_for(o);
+            float hi[16], mid[16];
+            tmem_ld16(tmem + lane_off + C::kColO + ob * C::kPCols + ch * 16, hi);
+            tmem_ld16(tmem + lane_off + C::kColO + ob * C::kPCols + N + ch * 16, mid);
+            tmem_ld_wait_for(hi);
+            tmem_ld_wait_for(mid);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) acc[ch * 16 + e] = o[e];
+            for (int e = 0; e < 16; ++e) acc[ch * 16 + e] = __fmaf_rn(mid[e], kMidScale, hi[e]);
           }
         }
         tc_fence_before_sync();

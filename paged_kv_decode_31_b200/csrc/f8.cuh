@@ -37,23 +37,12 @@ __device__ __forceinline__ uint32_t e4m3x2_of(__half2 v) {
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<uint32_t *>(&v)));
   return r;
 }
-__device__ __forceinline__ uint32_t e5m2x2_of(__half2 v) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<uint32_t *>(&v)));
-  return r;
-}
-// Back to fp16: exact (every value of either type is an fp16 value).
+// Back to fp16: exact (every e4m3 value is an fp16 value).
 __device__ __forceinline__ __half2 half2_of_e4m3x2(uint32_t v) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(v)));
   return *reinterpret_cast<__half2 *>(&r);
 }
-__device__ __forceinline__ __half2 half2_of_e5m2x2(uint32_t v) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(v)));
-  return *reinterpret_cast<__half2 *>(&r);
-}
-
 // A query row enters K Q^T as two 8-bit operands of one scale: the row times
 // 2^k, k chosen so that its largest magnitude lies in [128, 256), is
 // hi + lo with hi = e4m3(x) and lo = e5m2(x - hi).  A bf16 value has 8
@@ -72,26 +61,23 @@ __device__ __forceinline__ Split2 split_q(float x0, float x1) {
   return s;
 }
 
-// A probability in [0, 256] enters P V as three 8-bit operands of one scale:
-// p is rounded to fp16 (11 significant bits, off by at most 2^-11 relative)
-// and then taken apart, hi = e4m3(p), mid = e5m2(p - hi), lo = e5m2(p - hi -
-// mid).  The differences are exact in fp16; hi leaves at most 64 units of p's
-// last bit, mid at most 4 of those, which lo holds: the three sum to the fp16
-// value.  Only below 2^-6, where hi is subnormal, do the smallest steps show,
-// and the sum is then off by at most 2^-17, half of e5m2's smallest step (with
-// an e4m3 mid, whose smallest step is 2^-9, that would be 2^-14).
-struct Split3 {
-  uint32_t hi, mid, lo;
+// A probability in [0, 256] enters P V as two e4m3 operands, hi = e4m3(p) and
+// mid = e4m3(16 (p - hi)), whose products are accumulated apart and joined as
+// hi + mid / 16 in fp32.  hi leaves at most 2^-4 of p's power of two, mid keeps
+// 4 bits of that: p is off by at most 2^-9 relative (5.9e-4 rms), half of what
+// rounding P to bf16 would do and a quarter of a bf16 output's own half step;
+// below 2^-6 by at most 2^-14, half of mid's smallest step.  (The differences
+// are taken from p rounded to fp16, 2^-11, which is below all of that.)
+struct SplitP {
+  uint32_t hi, mid;
 };
-__device__ __forceinline__ Split3 split_p(float p0, float p1) {
-  Split3 s;
-  __half2 r = __floats2half2_rn(p0, p1);
+__device__ __forceinline__ SplitP split_p(float p0, float p1) {
+  SplitP s;
+  const __half2 r = __floats2half2_rn(p0, p1);
   s.hi = e4m3x2_of(r);
-  r = __hsub2(r, half2_of_e4m3x2(s.hi));
-  s.mid = e5m2x2_of(r);
-  r = __hsub2(r, half2_of_e5m2x2(s.mid));
-  s.lo = e5m2x2_of(r);
+  s.mid = e4m3x2_of(__hmul2(__hsub2(r, half2_of_e4m3x2(s.hi)), __floats2half2_rn(16.f, 16.f)));
   return s;
 }
+constexpr float kMidScale = 0.0625f;
 
 }  // namespace pkv

@@ -79,7 +79,7 @@ int launch_split_q8(const Q8Params &p, const CUtensorMap &mk, const CUtensorMap 
   const int grid = p.n_units < sm_count(dev) ? p.n_units : sm_count(dev);
   Q8Params pp = p;
   pp.sched = p.n_units <= C::kSchedScratch ? 1 : 0;
-  kern<<<grid, kThreads, C::kSmemBytes, s>>>(pp, mk, mv);
+  kern<<<grid, kQ8Threads, C::kSmemBytes, s>>>(pp, mk, mv);
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
