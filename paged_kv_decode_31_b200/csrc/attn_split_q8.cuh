@@ -5,18 +5,21 @@
 // tokens and KV head (f8.cuh).  Units, splits, tiles, schedule, roles and the
 // merge are those of attn_split.cuh; what differs is the arithmetic of a tile,
 // which runs on the 8-bit tensor-core path without ever widening the cache:
-//   S^T   = K8 * [q_hi + q_lo]^T   (kind::f8f6f4, M = 128 tokens, N = rows)
-//           with the query row taken apart exactly into two 8-bit operands
-//           of one scale (split_q), so S is q . k8 to fp32 accumulation;
+//   S^T   = K8 * [q_hi | q_lo]^T   (kind::f8f6f4, M = 128 tokens), the query
+//           row taken apart exactly into two 8-bit operands side by side
+//           (split_q) and S = S_hi + S_lo / 16, q . k8 to fp32 accumulation;
 //   w     = S * (c 2^-k 2^ek) + ev, per token: ek and ev are the exponents of
 //           its K and V scales, k the query row's, c = softmax scale * log2 e.
 //           w is the base-2 score plus the log of the V scale, so 2^w weighs
 //           the token's 8-bit V directly;
+//   (two tiles at a time from here on, 256 tokens, a thread holding a token of
+//   each: the chain of reductions, barriers and fences is latency, and its
+//   length hardly depends on how much it carries)
 //   m     the row's running reference (-inf at the split's start) rises to
 //           max(w) - kRefDrop when max(w) > m + 8; P = 2^(w - m) is then at
 //           most 2^8 and at least 2^(8 - kRefSlack) for the largest token;
-//   O^T  += V8^T * [P_hi | P_mid]^T, P as two 8-bit operands side by side
-//           (split_p), joined as O_hi + O_mid / 16 at the split's end;
+//   O^T  += V8^T * [P_hi | P_mid | P_lo]^T, P as three 8-bit operands side by
+//           side (split_p), joined (join_p) at the split's end;
 //   l     = sum of 2^(w - ev - m) = P 2^-ev over the tokens, in fp32.
 // (m, l, O) is a partial in the form the merge folds: out = O / l and lse =
 // (m + log2 l) ln 2.  Folding the V scale into the exponent keeps every
@@ -35,13 +38,13 @@
 
 namespace pkv {
 
-constexpr int kQ8Threads = 512;  // attn_split.cuh's roles, and
-constexpr int kPvWarp = 15;      // a second MMA issuer, for P.V
-
 // P <= 2^8 fits e4m3 (448); the reference moves when the largest token passes
 // it, and then to 2^kRefDrop below that token, so a row's largest P stays in
-// [2^kRefDrop, 2^8] and rescaling O stays rare.
-constexpr float kRefTop = 8.f, kRefDrop = 6.f;
+// [2^kRefDrop, 2^8] (p's smallest step, 2^-18, is then at most 2^-20 of it).
+// Each move waits for the P.V under way and rescales O, 6000 cycles without a
+// new tile: with 6 for kRefDrop moves in the first tiles of every split cost a
+// third of the time.
+constexpr float kRefTop = 8.f, kRefDrop = 2.f;
 
 struct Q8Params : AttnParams {
   const uint8_t *k_sc, *v_sc;  // scale bytes of (block, KV head)
@@ -49,60 +52,104 @@ struct Q8Params : AttnParams {
   int box_shift;               // log2(box_slots)
 };
 
-template <int D, int N, int NS>
+// Roles: NW softmax warpgroups that take the pairs of tiles in turn, the
+// correction + epilogue warpgroup, a warp for what a unit needs (table, scales,
+// Q), kLoaders warps for K and V, one each for QK^T (+ TMEM owner) and P.V.
+// N: rows that a unit can hold, 4, 8 or 16 -- the smallest that holds the call's
+// (everything per row is unrolled over it: with 16 throughout, 4 rows ran 900
+// instructions of which they needed a third, past the instruction cache).
+template <int D, int N, int NSK, int NSV>
 struct Q8Cfg {
   static_assert(D == 64 || D == 128, "head_dim 64 or 128");
-  static_assert(N == 16 || N == 64, "rows per tile");
-  static constexpr int kD = D, kN = N, kNS = NS, kQB = 2;
+  static_assert(N == 4 || N == 8 || N == 16, "rows per unit");
+  static constexpr int kD = D, kN = N, kQB = 2;
+  static constexpr int kNW = 2;
+  static constexpr int kNP = 2;                // P^T buffers (a pair of tiles each)
+  static constexpr int kCorr0 = 4 * kNW;       // first correction warp
+  // A 16-row box takes the TMA unit 100 cycles, but one warp only gets a box
+  // out every 145; with two warps each for K and V, on alternate stages, the
+  // unit's queue stays full (loads alone: 3.1 TB/s for 16-token blocks with
+  // one warp, 4.3 with two, 5.7 with four).
+  static constexpr int kLoaders = 4;
+  static constexpr int kPrepW = kCorr0 + 4, kLoadW = kCorr0 + 5, kQkW = kLoadW + kLoaders, kPvW = kQkW + 1;
+  static constexpr int kWarps = kPvW + 1;
+  static constexpr int kUS = 3;                // units whose table and scales are in shared memory
   static constexpr int kKVBytes = kTileTokens * D;     // one K (or V) tile, rows of D bytes
   static constexpr uint32_t kLayout = D == 128 ? kLayoutSw128 : kLayoutSw64;
   static constexpr int kAtom = 8 * D;                  // bytes of 8 rows, the swizzle's period
-  static constexpr int kQPiece = N * D;                // q_hi, then q_lo
-  static constexpr int kQBytes = 2 * kQPiece;
-  static constexpr int kPCols = 2 * N;                 // P^T columns: N hi, then N mid
-  static constexpr int kPBytes = kTileTokens * kPCols;
+  static constexpr int kQCols = N == 16 ? 32 : 16;     // S^T columns: N hi, N lo (and padding)
+  static constexpr int kQBytes = kQCols * D;
+  static constexpr int kPCols = N == 4 ? 16 : N == 8 ? 32 : 48;  // P^T columns: N hi, mid, lo (and padding)
+  static constexpr int kPTile = kTileTokens * kPCols;
+  static constexpr int kPBytes = 2 * kPTile;
   static constexpr int kPKGroup = (kPCols / 16) * 128;  // P^T stride between 8-token groups
   static constexpr int kSB = 4;                         // S^T buffers
+  // Scale bytes per tile.  K of tile g + kSC is issued when K of tile g + kSC -
+  // NSK is used, so its S^T buffer was free: tile g + kSC - NSK - kSB's softmax
+  // had read its S^T, and its scales before that.
+  static constexpr int kSC = 16;
+  static_assert(NSK + kSB <= kSC, "a slot of scale bytes is rewritten after its tile's softmax read it");
   static constexpr int kOffK = 0;
-  static constexpr int kOffV = NS * kKVBytes;
-  static constexpr int kOffQ = 2 * NS * kKVBytes;
+  static constexpr int kOffV = NSK * kKVBytes;
+  static constexpr int kOffQ = (NSK + NSV) * kKVBytes;
   static constexpr int kOffP = kOffQ + kQB * kQBytes;
-  static constexpr int kOffSmall = kOffP + 2 * kPBytes;
+  static constexpr int kOffSmall = kOffP + kNP * kPBytes;
   static constexpr int kSchedScratch = kOffSmall - kOffQ;  // bytes free at kernel start
+  // a unit's query rows as they are in memory
+  static constexpr int kRawBytes = N * D * 2;
   struct Small {
-    uint64_t full_k[NS], empty_k[NS], full_v[NS], empty_v[NS];
-    uint64_t s_full[kSB], s_free[kSB], p_full[2], o_full[2], stat_free[2];
-    uint64_t m_full[2];     // [tile parity]: the tile's running references are published and
-                            // those of the tile before it read
+    __align__(16) uint8_t raw_q[kRawBytes];
+    uint64_t full_k[NSK], empty_k[NSK], full_v[NSV], empty_v[NSV];
+    uint64_t sc_full[kSC];  // [tile % kSC]: the tile's scale bytes are staged
+    uint64_t tab_full[kUS], tab_free[kUS];  // [unit % kUS]: its table and scales are there; are used
+    uint64_t s_full[kSB], s_free[kSB], p_full[kNP], o_full[kNP], stat_free[kNP];
+    uint64_t m_full[2];     // [pair parity]: the pair's running references are published and
+                            // those of the pair before it read
     uint64_t unit_done[2];  // [O buffer]: a unit's last P.V completed
     uint64_t o_free[2];     // [O buffer]: the unit's O is read out
     uint64_t q_full[kQB], q_empty[kQB], drain[2];
     uint32_t tmem_base;
     int abort_any;
-    __align__(16) float wmax[2][2][4][N];  // [softmax warpgroup][tile parity][warp][row]
-    __align__(16) float wsum[2][4][N];     // [buffer][warp][row]: per-warp sums
-    float mnew[2][N];                      // [buffer][row]: the reference after the tile
-    __align__(16) float mw[2][4][N];       // [softmax warpgroup][warp][row]: the warp's copy of it
-    __align__(16) float aw[2][4][N];       // ... and of the factor
-    float scl[2][N];                       // [buffer][row]: factor O and l take before it
-    float mrun[2][N];                      // [tile parity][row]: mnew for the next tile
+    __align__(16) float wmax[kNW][2][4][N];  // [softmax warpgroup][its pair's parity][warp][row]
+    __align__(16) float wsum[kNP][4][N];   // [buffer][warp][row]: per-warp sums
+    float mnew[kNP][N];                    // [buffer][row]: the reference after the pair
+    __align__(16) float mw[kNW][4][N];     // [softmax warpgroup][warp][row]: the warp's copy of it
+    __align__(16) float aw[kNW][4][N];     // ... and of the factor
+    float scl[kNP][N];                     // [buffer][row]: factor O and l take before it
+    float mrun[2][N];                      // [pair parity][row]: mnew for the next pair
     __align__(16) float rowf[kQB][N];      // [Q buffer][row]: c 2^-k
     float fin_m[N], fin_l[N];              // each row's (m, l) for the direct final write
     int sched_list[kSchedMaxMine];
     int sched_meta[kSchedMaxMine][3];
+    Unit units[kSchedMaxMine];             // this CTA's units, worked out once
     int sched_hist[kSchedHist], sched_start[kSchedBuckets];
     int sched_count;
-    __align__(16) int lim[2][N];           // [softmax warpgroup][row]: key limit
-    int tab[2][2][kSplitTokens / 16];      // [producer][unit parity]: block-table entries
-    uint8_t sctab[2][2][kSplitTokens / 16];  // [unit parity][K, V]: the entries' scale bytes
-    uint8_t sc[NS][2][8];                  // [stage][K, V][box]: scale bytes of the stage's tile
+    __align__(16) int lim[kNW][N];         // [softmax warpgroup][row]: key limit
+    int tab[kUS][kSplitTokens / 16];       // [unit % kUS]: block-table entries
+    uint16_t sctab[kUS][kSplitTokens / 16];  // [unit % kUS]: the entries' scale bytes, K | V << 8
+    uint16_t sc[kSC][8];                   // [tile % kSC][box]: the tile's scale bytes
   };
   static constexpr int kSmemBytes = kOffSmall + static_cast<int>(sizeof(Small)) + 1024;
-  // TMEM: S^T (N columns) x kSB buffers, then O^T (hi and mid, 2N columns) x 2
-  // buffers (alternate units)
-  static constexpr int kTmemCols = N == 16 ? 128 : 512;
-  static constexpr uint32_t kColO = kSB * N;
+  // TMEM: S^T (hi and lo) x kSB buffers, then O^T (hi, mid and lo) x 2 buffers
+  // (alternate units)
+  static constexpr uint32_t kColO = kSB * kQCols;
+  static constexpr int kTmemCols = kColO + 2 * kPCols <= 128 ? 128 : 256;
+  static_assert(kColO + 2 * kPCols <= kTmemCols, "TMEM columns");
 };
+
+// C consecutive columns of the thread's TMEM lane (C a multiple of 8).
+template <int C>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float *v) {
+#pragma unroll
+  for (int c = 0; c + 16 <= C; c += 16) tmem_ld16(taddr + c, *reinterpret_cast<float(*)[16]>(v + c));
+  if constexpr (C % 16 == 8) tmem_ld8(taddr + C - 8, v + C - 8);
+}
+template <int C>
+__device__ __forceinline__ void tmem_ld_cols_wait(float *v) {
+#pragma unroll
+  for (int c = 0; c + 16 <= C; c += 16) tmem_ld_wait_for(*reinterpret_cast<float(*)[16]>(v + c));
+  if constexpr (C % 16 == 8) tmem_ld_wait_for8(v + C - 8);
+}
 
 // A scale byte, held to the range that the arithmetic covers (a byte outside
 // it is reported).
@@ -114,63 +161,52 @@ __device__ __forceinline__ int checked_scale(int byte, int32_t *err) {
   return byte;
 }
 
-// A unit's block-table entries and their scale bytes on the way to shared
-// memory, a lane's share in registers: the loads of the next unit go out
-// before the tiles of this one are issued and are used after them.  (Under a
-// saturated memory system a load takes microseconds, and at a unit's boundary
-// every tile behind it waits: loading there cost 10 us per unit.)
+// A unit's block-table entries, their scale bytes and its query rows come from
+// a warp of their own, units ahead of the tiles: under a saturated memory
+// system a load takes microseconds, and in a producer warp every tile behind
+// it waits (10 us per unit, a third of the time).
 constexpr int kTabBatch = kSplitTokens / 16 / 32;  // entries per lane at most
-
-struct TabRegs {
-  int blk[kTabBatch], kb[kTabBatch], vb[kTabBatch];
-};
 
 __device__ __forceinline__ int tab_entries(const Q8Params &p, const Unit &x) {
   const int ntok = min(kSplitTokens, x.lim_max - x.tok0);
   return (ntok + (1 << p.block_shift) - 1) >> p.block_shift;
 }
 
-__device__ __forceinline__ void load_tab(const Q8Params &p, const Unit &x, TabRegs &r, int lane) {
+// (asynchronous: complete after cp_async_wait<0> and a __syncwarp)
+__device__ __forceinline__ void fetch_tab(const Q8Params &p, const Unit &x, int *tab, int lane) {
   const int nent = tab_entries(p, x), first = x.tok0 >> p.block_shift;
-#pragma unroll
-  for (int i = 0; i < kTabBatch; ++i) {
-    const int e = lane + 32 * i;
-    r.blk[i] = kPastWidth;
-    if (e < nent && first + e < p.max_blocks_per_seq)
-      r.blk[i] = __ldg(p.block_table + x.b * p.bt_stride + first + e);
+  const int32_t *src = p.block_table + x.b * p.bt_stride + first;
+#pragma unroll 1
+  for (int e = lane; e < nent; e += 32) {
+    if (first + e < p.max_blocks_per_seq)
+      cp_async4(tab + e, src + e);
+    else
+      tab[e] = kPastWidth;
   }
 }
 
-__device__ __forceinline__ void load_scales(const Q8Params &p, const Unit &x, TabRegs &r) {
+__device__ __forceinline__ void load_scales(const Q8Params &p, const Unit &x, const int *tab,
+                                            int (&kb)[kTabBatch], int (&vb)[kTabBatch], int lane) {
+  const int nent = tab_entries(p, x);
 #pragma unroll
   for (int i = 0; i < kTabBatch; ++i) {
-    const int64_t blk = r.blk[i];
-    r.kb[i] = r.vb[i] = 127;
+    const int64_t blk = lane + 32 * i < nent ? tab[lane + 32 * i] : -1;
+    kb[i] = vb[i] = 127;
     if (blk >= 0 && blk < p.num_blocks) {  // (kPastWidth is negative)
-      r.kb[i] = __ldg(p.k_sc + blk * p.ksc_sb + x.kvh * p.ksc_sh);
-      r.vb[i] = __ldg(p.v_sc + blk * p.vsc_sb + x.kvh * p.vsc_sh);
+      kb[i] = ldg_here(p.k_sc + blk * p.ksc_sb + x.kvh * p.ksc_sh);
+      vb[i] = ldg_here(p.v_sc + blk * p.vsc_sb + x.kvh * p.vsc_sh);
     }
   }
 }
 
-__device__ __forceinline__ void put_tab(const Q8Params &p, const Unit &x, const TabRegs &r, int *tab,
-                                        int lane) {
-  const int nent = tab_entries(p, x);
-#pragma unroll
-  for (int i = 0; i < kTabBatch; ++i)
-    if (lane + 32 * i < nent) tab[lane + 32 * i] = r.blk[i];
-}
-
-__device__ __forceinline__ void put_scales(const Q8Params &p, const Unit &x, const TabRegs &r,
-                                           uint8_t (*sctab)[kSplitTokens / 16], int lane) {
+__device__ __forceinline__ void put_scales(const Q8Params &p, const Unit &x, const int (&kb)[kTabBatch],
+                                           const int (&vb)[kTabBatch], uint16_t *sctab, int lane) {
   const int nent = tab_entries(p, x);
 #pragma unroll
   for (int i = 0; i < kTabBatch; ++i) {
     const int e = lane + 32 * i;
-    if (e < nent) {
-      sctab[0][e] = static_cast<uint8_t>(checked_scale(r.kb[i], p.err));
-      sctab[1][e] = static_cast<uint8_t>(checked_scale(r.vb[i], p.err));
-    }
+    if (e < nent)
+      sctab[e] = static_cast<uint16_t>(checked_scale(kb[i], p.err) | (checked_scale(vb[i], p.err) << 8));
   }
 }
 
@@ -186,22 +222,18 @@ __device__ __forceinline__ int swz16(int r, int c) {
 // warp takes 256 / D rows.  Rows past x.rows keep whatever the buffer holds:
 // their columns of S^T are never used.
 template <int D>
-__device__ __forceinline__ uint4 load_q_pass(const Q8Params &p, const Unit &x, int pass, int lane) {
-  constexpr int kLanes = D / 8;
-  const int c = pass * (32 / kLanes) + lane / kLanes;
-  if (c >= x.rows) return make_uint4(0u, 0u, 0u, 0u);
+__device__ __forceinline__ const uint4 *q_row(const Q8Params &p, const Unit &x, int c) {
   const int r = x.row0 + c;
   const int i = r / p.G, g = r - i * p.G;
-  return __ldg(reinterpret_cast<const uint4 *>(p.q + q_tok_off(p, x, i) +
-                                               static_cast<int64_t>(x.kvh * p.G + g) * p.q_sh) +
-               lane % kLanes);
+  return reinterpret_cast<const uint4 *>(p.q + q_tok_off(p, x, i) +
+                                         static_cast<int64_t>(x.kvh * p.G + g) * p.q_sh);
 }
 
 template <int D, int N>
-__device__ __forceinline__ void put_q_pass(const Q8Params &p, uint4 v, int pass, uint8_t *qdst,
+__device__ __forceinline__ void put_q_pass(const Q8Params &p, uint4 v, int c, uint8_t *qdst,
                                            float *rowf, int lane) {
   constexpr int kLanes = D / 8;
-  const int ch = lane % kLanes, c = pass * (32 / kLanes) + lane / kLanes;
+  const int ch = lane % kLanes;
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t top = 0;  // largest magnitude as bits: ordered like the values, NaN and inf on top
 #pragma unroll
@@ -225,159 +257,181 @@ __device__ __forceinline__ void put_q_pass(const Q8Params &p, uint4 v, int pass,
     hi[e] = s.hi;
     lo[e] = s.lo;
   }
-  uint8_t *dst = qdst + swz16<D>(c, ch >> 1) + (ch & 1) * 8;
-  *reinterpret_cast<uint2 *>(dst) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-  *reinterpret_cast<uint2 *>(dst + N * D) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+  *reinterpret_cast<uint2 *>(qdst + swz16<D>(c, ch >> 1) + (ch & 1) * 8) =
+      make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+  *reinterpret_cast<uint2 *>(qdst + swz16<D>(N + c, ch >> 1) + (ch & 1) * 8) =
+      make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
   if (ch == 0) rowf[c] = __fmul_rn(p.cscale, __int_as_float((127 - k) << 23));
 }
 
-// One producer warp (K and the query rows, or V and the scales); the stage
-// ring, the bounded waits and the exit are attn_split.cuh's produce().
+// The units of this CTA: from shared memory, where they were worked out once
+// (the divisions of unit_make in every role would be most of the kernel's
+// code), or, when they are more than fit there, by a function call.
+struct Sched8 {
+  const Unit *units;
+  int count;
+};
+
+template <int N>
+__device__ __noinline__ Unit strided_unit(const Q8Params &p, int k) {
+  return unit_at<N>(p, static_cast<int>(blockIdx.x) + k * static_cast<int>(gridDim.x));
+}
+
+template <int N>
+__device__ __forceinline__ Unit unit8(const Q8Params &p, const Sched8 &sc, int k) {
+  return sc.units ? sc.units[k] : strided_unit<N>(p, k);
+}
+
+// First unit with tiles at or after `from`, or -1.
+template <int N>
+__device__ __forceinline__ int next_unit8(const Q8Params &p, const Sched8 &sc, int from, Unit &out) {
+  for (int k = from; k < sc.count; ++k) {
+    out = unit8<N>(p, sc, k);
+    if (out.n_tiles > 0) return k;
+  }
+  return -1;
+}
+
+// The preparing warp: for every unit with tiles, in order, its table and scale
+// bytes (slot unit % kUS) and its query rows (buffer unit % kQB).
 template <class C>
-__device__ __forceinline__ void produce_q8(const Q8Params &p, const CUtensorMap *map, uint8_t *smem,
-                                           typename C::Small *sm, uint64_t *full, uint64_t *empty,
-                                           int (*tabs)[kSplitTokens / 16], uint32_t dst_off,
-                                           bool is_k, int lane, volatile int *abort_any,
-                                           const Sched &sc) {
-  constexpr int D = C::kD, N = C::kN, NS = C::kNS, QB = C::kQB;
+__device__ __forceinline__ void prepare_q8(const Q8Params &p, uint8_t *smem, typename C::Small *sm,
+                                           int lane, volatile int *abort_any, const Sched8 &sc) {
+  constexpr int D = C::kD, N = C::kN, QB = C::kQB, US = C::kUS;
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes per query row, rows per pass
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    bool ok = true;
+    if (lane == 0) ok = mbar_wait_call(bar, parity, abort_any, p.wait_ns);
+    return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+  };
+  Unit cur, nxt;
+  int k = next_unit8<N>(p, sc, 0, cur);
+  if (k >= 0) fetch_tab(p, cur, sm->tab[0], lane);
+  cp_async_commit();
+  int kb[kTabBatch], vb[kTabBatch];
+  for (int ui = 0; k >= 0; ++ui) {
+    const int nk = next_unit8<N>(p, sc, k + 1, nxt);
+    // this unit's query rows, and the next unit's table
+#pragma unroll 1
+    for (int c = lane / kLanes; c < cur.rows; c += kRows)
+      cp_async16(sm->raw_q + c * D * 2 + (lane % kLanes) * 16, q_row<D>(p, cur, c) + lane % kLanes, 16);
+    cp_async_commit();
+    if (nk >= 0) {
+      const int n = ui + 1;
+      if (!wait(&sm->tab_free[n % US], ((n / US) & 1) ^ 1)) break;
+      fetch_tab(p, nxt, sm->tab[n % US], lane);
+    }
+    cp_async_commit();
+    cp_async_wait<2>();  // this unit's table
+    __syncwarp();
+    load_scales(p, cur, sm->tab[ui % US], kb, vb, lane);
+    put_scales(p, cur, kb, vb, sm->sctab[ui % US], lane);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm->tab_full[ui % US]);
+    // Q goes into the buffer of the unit two before this one, once that unit's
+    // last QK^T and its epilogue (staged there) are done
+    if (!wait(&sm->q_empty[ui % QB], ((ui / QB) & 1) ^ 1)) break;
+    cp_async_wait<1>();
+    __syncwarp();
+    uint8_t *dst = smem + C::kOffQ + (ui % QB) * C::kQBytes;
+#pragma unroll 1
+    for (int c0 = 0; c0 < cur.rows; c0 += kRows) {
+      const int c = c0 + lane / kLanes;
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (c < cur.rows)
+        v = *reinterpret_cast<const uint4 *>(sm->raw_q + c * D * 2 + (lane % kLanes) * 16);
+      put_q_pass<D, N>(p, v, c, dst, sm->rowf[ui % QB], lane);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm->q_full[ui % QB]);
+    cur = nxt;
+    k = nk;
+  }
+  cp_async_wait<0>();
+}
+
+// One loading warp: K (with the tiles' scale bytes) or V of the tiles that go
+// to its stages -- even or odd ones: a stage has one warp, which then waits for
+// every use of it in turn (a parity wait cannot tell a use from the one two
+// before it).  Eight lanes (boxes) of a tile at once.  The bounded waits and
+// the exit are those of attn_split.cuh's produce().
+template <class C, int NS>
+__device__ __forceinline__ void load_q8(const Q8Params &p, const CUtensorMap *map, uint8_t *smem,
+                                        typename C::Small *sm, uint64_t *full, uint64_t *empty,
+                                        uint32_t dst_off, bool is_k, int part, int lane,
+                                        volatile int *abort_any, const Sched8 &sc) {
+  constexpr int D = C::kD, N = C::kN, US = C::kUS;
+  const int bmask = (1 << p.block_shift) - 1;
   if (lane == 0) tma_prefetch_desc(map);
-  int last_gi[NS];
-#pragma unroll
-  for (int i = 0; i < NS; ++i) last_gi[i] = -1;
+  const uint32_t box_bytes = static_cast<uint32_t>(p.box_slots * D);
+  int gi = 0;
   bool failed = false;
-  Unit cur;
-  int cu = next_unit<N>(p, sc, 0, cur);
-  if (cu >= 0) {
-    const int bmask = (1 << p.block_shift) - 1;
-    int ui = 0, gi = 0;
-    constexpr int kPasses = N * D / 256;
-    constexpr bool kEarly = kPasses <= 8;  // the next unit's Q waits in registers too
-    TabRegs tr;
-    uint4 qr[kEarly ? kPasses : 1];
-    auto load_q = [&](const Unit &u) {
-      if constexpr (kEarly) {
-#pragma unroll
-        for (int i = 0; i < kPasses; ++i)
-          if (i * (256 / D) < u.rows) qr[i] = load_q_pass<D>(p, u, i, lane);
+  Unit x;
+  for (int k = next_unit8<N>(p, sc, 0, x), ui = 0; k >= 0 && !failed;
+       k = next_unit8<N>(p, sc, k + 1, x), ++ui) {
+    bool okt = true;
+    if (lane == 0) okt = mbar_wait_call(&sm->tab_full[ui % US], (ui / US) & 1, abort_any, p.wait_ns);
+    if (!__shfl_sync(0xffffffffu, okt ? 1 : 0, 0)) break;
+    const int *tab = sm->tab[ui % US];
+    const uint16_t *sct = sm->sctab[ui % US];
+    for (int j = 0; j < x.n_tiles; ++j, ++gi) {
+      const int st = gi % NS;
+      if ((st & 1) != part) continue;
+      bool okw = true;
+      if (lane == 0) okw = mbar_wait_call(&empty[st], ((gi / NS) & 1) ^ 1, abort_any, p.wait_ns);
+      if (!__shfl_sync(0xffffffffu, okw ? 1 : 0, 0)) {
+        failed = true;
+        break;
       }
-    };
-    auto put_q = [&](const Unit &u, int ord) {
-      uint8_t *dst = smem + C::kOffQ + (ord % QB) * C::kQBytes;
-      float *rowf = sm->rowf[ord % QB];
-      if constexpr (kEarly) {
-#pragma unroll
-        for (int i = 0; i < kPasses; ++i)
-          if (i * (256 / D) < u.rows) put_q_pass<D, N>(p, qr[i], i, dst, rowf, lane);
-      } else {
-#pragma unroll 4
-        for (int i = 0; i < kPasses; ++i)
-          if (i * (256 / D) < u.rows)
-            put_q_pass<D, N>(p, load_q_pass<D>(p, u, i, lane), i, dst, rowf, lane);
+      const int tok0 = x.tok0 + j * kTileTokens;
+      const int nbox = (min(kTileTokens, x.lim_max - tok0) + p.box_slots - 1) >> p.box_shift;
+      const int tok = tok0 + (lane << p.box_shift);
+      int blk = 0, errs = 0;
+      bool load = false;
+      if (lane < nbox) {
+        const int e = (tok - x.tok0) >> p.block_shift;
+        blk = tab[e];
+        if (blk == kPastWidth)
+          errs = kErrTableWidth;
+        else if (blk < 0 || static_cast<int64_t>(blk) >= p.num_blocks)
+          errs = kErrBadBlock;
+        else
+          load = true;
+        if (is_k) sm->sc[gi % C::kSC][lane] = sct[e];
       }
-      fence_proxy_async_smem();
+      const uint32_t loads = __ballot_sync(0xffffffffu, load);
+      __syncwarp();  // (the scale bytes, before the arrival)
+      if (lane == 0) {
+        if (is_k) mbar_arrive(&sm->sc_full[gi % C::kSC]);
+        mbar_arrive_expect_tx(&full[st], __popc(loads) * box_bytes);
+      }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm->q_full[ord % QB]);
-    };
-    load_tab(p, cur, tr, lane);
-    if (is_k) load_q(cur);
-    put_tab(p, cur, tr, tabs[0], lane);
-    if (is_k) {
-      put_q(cur, 0);
-    } else {
-      load_scales(p, cur, tr);
-      put_scales(p, cur, tr, sm->sctab[0], lane);
+      if (load) {
+        const int slot = tok & bmask;
+        tma_load_4d(smem + dst_off + st * C::kKVBytes + lane * box_bytes, map, &full[st], 0,
+                    p.map_head_first ? x.kvh : slot, p.map_head_first ? slot : x.kvh, blk);
+      }
+      if (errs && p.err) atomicOr(p.err, errs);
     }
     __syncwarp();
-    while (true) {
-      Unit nxt;
-      const int nu = next_unit<N>(p, sc, cu + 1, nxt);
-      if (nu >= 0) {
-        load_tab(p, nxt, tr, lane);
-        if (is_k) load_q(nxt);
-      }
-      // V: the entries have arrived a few tiles on, and their scales are
-      // fetched behind the remaining ones
-      const int j_scales = min(cur.n_tiles - 1, 4);
-      const int *tab = tabs[ui & 1];
-      for (int j = 0; j < cur.n_tiles && !failed; ++j, ++gi) {
-        const int st = gi % NS;
-        bool okw = true;
-        if (lane == 0) okw = mbar_wait(&empty[st], ((gi / NS) & 1) ^ 1, abort_any, p.wait_ns);
-        if (!__shfl_sync(0xffffffffu, okw ? 1 : 0, 0)) {
-          failed = true;
-          break;
-        }
-        const int tok0 = cur.tok0 + j * kTileTokens;
-        const int nvalid = min(kTileTokens, cur.lim_max - tok0);
-        const int nbox = (nvalid + p.box_slots - 1) >> p.box_shift;
-        int errs = 0;
-        if (lane < nbox) {
-          const int tok = tok0 + (lane << p.box_shift);
-          const int e = (tok - cur.tok0) >> p.block_shift;
-          const int blk = tab[e];
-          if (blk == kPastWidth) {
-            errs = kErrTableWidth;
-          } else if (blk < 0 || static_cast<int64_t>(blk) >= p.num_blocks) {
-            errs = kErrBadBlock;
-          } else {
-            uint8_t *d0 = smem + dst_off + st * C::kKVBytes + (lane << p.box_shift) * D;
-            const int slot = tok & bmask;
-            const int c1 = p.map_head_first ? cur.kvh : slot;
-            const int c2 = p.map_head_first ? slot : cur.kvh;
-            mbar_expect_tx(&full[st], static_cast<uint32_t>(p.box_slots * D));
-            tma_load_4d(d0, map, &full[st], 0, c1, c2, blk);
-          }
-          if (!is_k) {
-            sm->sc[st][0][lane] = sm->sctab[ui & 1][0][e];
-            sm->sc[st][1][lane] = sm->sctab[ui & 1][1][e];
-          }
-        }
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&full[st]);
-          last_gi[st] = gi;
-        }
-        if (errs && p.err) atomicOr(p.err, errs);
-        if (!is_k && nu >= 0 && j == j_scales) load_scales(p, nxt, tr);
-      }
-      if (failed || nu < 0) break;
-      // (the other parity's entries were last read for the unit before this one)
-      put_tab(p, nxt, tr, tabs[(ui + 1) & 1], lane);
-      if (!is_k) put_scales(p, nxt, tr, sm->sctab[(ui + 1) & 1], lane);
-      // The next unit's Q goes into the buffer of the unit before this one,
-      // once its last QK^T and its epilogue (staged there) are done; see
-      // produce() for why the wait comes after this unit's last tile.
-      if (is_k) {
-        const int qb = (ui + 1) % QB;
-        bool okq = true;
-        if (lane == 0) okq = mbar_wait(&sm->q_empty[qb], (((ui + 1) / QB) & 1) ^ 1, abort_any, p.wait_ns);
-        if (!__shfl_sync(0xffffffffu, okq ? 1 : 0, 0)) {
-          failed = true;
-          break;
-        }
-        put_q(nxt, ui + 1);
-      }
-      __syncwarp();
-      ++ui;
-      cur = nxt;
-      cu = nu;
-    }
+    if (lane == 0) mbar_arrive(&sm->tab_free[ui % US]);
   }
   if (lane == 0) {
-    // every copy this warp issued lands before the CTA exits (bounded)
+    // every copy this warp issued lands before the CTA exits (bounded): the
+    // last tile of each of its stages
     volatile int no_abort = 0;
-#pragma unroll
-    for (int i = 0; i < NS; ++i)
-      if (last_gi[i] >= 0) mbar_wait(&full[i], (last_gi[i] / NS) & 1, &no_abort);
+    for (int g = max(gi - NS, 0); g < gi; ++g)
+      if ((g % NS & 1) == part) mbar_wait_call(&full[g % NS], (g / NS) & 1, &no_abort);
   }
 }
 
-template <int D, int N, int NS>
-__global__ void __launch_bounds__(kQ8Threads, 1)
+template <int D, int N, int NSK, int NSV>
+__global__ void __launch_bounds__(32 * Q8Cfg<D, N, NSK, NSV>::kWarps, 1)
     attn_split_q8_kernel(const __grid_constant__ Q8Params p,
                          const __grid_constant__ CUtensorMap map_k,
                          const __grid_constant__ CUtensorMap map_v) {
-  using C = Q8Cfg<D, N, NS>;
+  using C = Q8Cfg<D, N, NSK, NSV>;
   constexpr int QB = C::kQB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -388,20 +442,29 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
   volatile int *abort_any = &sm->abort_any;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < NS; ++i) {
+    for (int i = 0; i < NSK; ++i) {
       mbar_init(&sm->full_k[i], 1);
       mbar_init(&sm->empty_k[i], 1);
+    }
+    for (int i = 0; i < NSV; ++i) {
       mbar_init(&sm->full_v[i], 1);
       mbar_init(&sm->empty_v[i], 1);
+    }
+    for (int i = 0; i < C::kSC; ++i) mbar_init(&sm->sc_full[i], 1);
+    for (int i = 0; i < C::kUS; ++i) {
+      mbar_init(&sm->tab_full[i], 1);
+      mbar_init(&sm->tab_free[i], C::kLoaders);
     }
     for (int i = 0; i < C::kSB; ++i) {
       mbar_init(&sm->s_full[i], 1);
       mbar_init(&sm->s_free[i], 4);   // one arrival per warp of a softmax warpgroup
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::kNP; ++i) {
       mbar_init(&sm->p_full[i], 4);   // one arrival per warp of a softmax warpgroup
       mbar_init(&sm->o_full[i], 1);
       mbar_init(&sm->stat_free[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&sm->m_full[i], 4);   // one arrival per warp of a softmax warpgroup
       mbar_init(&sm->unit_done[i], 1);
       mbar_init(&sm->o_free[i], 4);   // one arrival per correction warp
@@ -412,41 +475,38 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     sm->abort_any = 0;
     fence_barrier_init();
   }
-  if (warp == kMmaWarp) tmem_alloc(&sm->tmem_base, C::kTmemCols);
+  if (warp == C::kQkW) tmem_alloc(&sm->tmem_base, C::kTmemCols);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = sm->tmem_base;
   const uint32_t sbase = smem_u32(smem);
   // the Q and P^T buffers are not in use yet: the schedule's scratch
-  Sched sc = strided_sched(p);
-  if (p.sched) {
-    build_schedule<N>(p, smem + C::kOffQ, C::kSchedScratch, sm->sched_hist, sm->sched_start,
-                      sm->sched_list, sm->sched_meta, &sm->sched_count);
-    if (sm->sched_count >= 0) {
-      sc = Sched{sm->sched_list, sm->sched_meta, sm->sched_count};
-    } else if (sc.count <= kSchedMaxMine) {
-      // nothing to balance: the stride-grid deal as a list, so that no role
-      // reads global memory between units
-      for (int k = threadIdx.x; k < sc.count; k += kQ8Threads) {
-        const int u = sc.unit(k), b = unit_seq(p, u);
-        sm->sched_list[k] = u;
-        sm->sched_meta[k][0] = __ldg(p.seqlens + b);
-        sm->sched_meta[k][1] = p.cu_q ? __ldg(p.cu_q + b) : 0;
-        sm->sched_meta[k][2] = p.cu_q ? __ldg(p.cu_q + b + 1) : 0;
-      }
+  Sched8 sc;
+  {
+    Sched deal = strided_sched(p);
+    if (p.sched) {
+      build_schedule<N>(p, smem + C::kOffQ, C::kSchedScratch, sm->sched_hist, sm->sched_start,
+                        sm->sched_list, sm->sched_meta, &sm->sched_count);
+      if (sm->sched_count >= 0) deal = Sched{sm->sched_list, sm->sched_meta, sm->sched_count};
+    }
+    sc = Sched8{deal.count <= kSchedMaxMine ? sm->units : nullptr, deal.count};
+    if (sc.units) {
+      for (int k = threadIdx.x; k < sc.count; k += blockDim.x) sm->units[k] = deal.get<N>(p, k);
       __syncthreads();
-      sc = Sched{sm->sched_list, sm->sched_meta, sc.count};
     }
   }
 
-  if (warp == kKWarp) {
-    produce_q8<C>(p, &map_k, smem, sm, sm->full_k, sm->empty_k, sm->tab[0], C::kOffK, true, lane,
-                  abort_any, sc);
-  } else if (warp == kVWarp) {
-    produce_q8<C>(p, &map_v, smem, sm, sm->full_v, sm->empty_v, sm->tab[1], C::kOffV, false, lane,
-                  abort_any, sc);
-  } else if (warp == kMmaWarp || warp == kPvWarp) {
+  if (warp == C::kPrepW) {
+    prepare_q8<C>(p, smem, sm, lane, abort_any, sc);
+  } else if (warp >= C::kLoadW && warp < C::kQkW) {
+    const int w = warp - C::kLoadW;
+    if (w < 2)
+      load_q8<C, NSK>(p, &map_k, smem, sm, sm->full_k, sm->empty_k, C::kOffK, true, w, lane, abort_any, sc);
+    else
+      load_q8<C, NSV>(p, &map_v, smem, sm, sm->full_v, sm->empty_v, C::kOffV, false, w - 2, lane,
+                      abort_any, sc);
+  } else if (warp == C::kQkW || warp == C::kPvW) {
     // ------------------------------------------------------------------
     // MMA issuers, one thread each: QK^T of every tile as soon as its K and a
     // S^T buffer are there, and P.V of every tile as soon as its P and V are.
@@ -455,38 +515,34 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     // tile's 32 KB take from memory.
     // ------------------------------------------------------------------
     if (lane == 0) {
-      const bool is_qk = warp == kMmaWarp;
-      // A = K tile, B = q_hi / q_lo (K-major); A = V^T, B = P^T (MN-major)
-      constexpr uint32_t kQkHi = idesc_f8(128, N, kFmtE4M3, kFmtE4M3, 0, 0);
-      constexpr uint32_t kQkLo = idesc_f8(128, N, kFmtE4M3, kFmtE5M2, 0, 0);
+      const bool is_qk = warp == C::kQkW;
+      // A = K tile, B = [q_hi | q_lo] (K-major); A = V^T, B = P^T (MN-major)
+      constexpr uint32_t kQk = idesc_f8(128, C::kQCols, kFmtE4M3, kFmtE4M3, 0, 0);
       constexpr uint32_t kPv = idesc_f8(128, C::kPCols, kFmtE4M3, kFmtE4M3, 1, 1);
-      int gi = 0, ui = 0;
+      int gi = 0, pi = 0, ui = 0;
       bool failed = false;
       for (int k = 0; k < sc.count && !failed; ++k) {
-        const Unit x = sc.get<N>(p, k);
+        const Unit x = unit8<N>(p, sc, k);
         if (x.n_tiles == 0) continue;
         if (is_qk) {
           const int qb = ui % QB;
-          if (!mbar_wait(&sm->q_full[qb], (ui / QB) & 1, abort_any, p.wait_ns)) {
+          if (!mbar_wait_call(&sm->q_full[qb], (ui / QB) & 1, abort_any, p.wait_ns)) {
             failed = true;
             break;
           }
           const uint64_t bh = smem_desc(sbase + C::kOffQ + qb * C::kQBytes, 16, C::kAtom, C::kLayout);
           for (int j = 0; j < x.n_tiles; ++j, ++gi) {
-            const int st = gi % NS, sb = gi % C::kSB;
-            if (!mbar_wait(&sm->full_k[st], (gi / NS) & 1, abort_any, p.wait_ns) ||
-                !mbar_wait(&sm->s_free[sb], ((gi / C::kSB) & 1) ^ 1, abort_any, p.wait_ns)) {
+            const int st = gi % NSK, sb = gi % C::kSB;
+            if (!mbar_wait_call(&sm->full_k[st], (gi / NSK) & 1, abort_any, p.wait_ns) ||
+                !mbar_wait_call(&sm->s_free[sb], ((gi / C::kSB) & 1) ^ 1, abort_any, p.wait_ns)) {
               failed = true;
               break;
             }
             tc_fence_after_sync();
             const uint64_t a = smem_desc(sbase + C::kOffK + st * C::kKVBytes, 16, C::kAtom, C::kLayout);
-            const uint32_t d = tmem + sb * N;
+            const uint32_t d = tmem + sb * C::kQCols;
 #pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk) {
-              umma_f8(d, a + kk * 2, bh + kk * 2, kQkHi, kk > 0 ? 1u : 0u);
-              umma_f8(d, a + kk * 2, bh + (C::kQPiece >> 4) + kk * 2, kQkLo, 1u);
-            }
+            for (int kk = 0; kk < D / 32; ++kk) umma_f8(d, a + kk * 2, bh + kk * 2, kQk, kk > 0 ? 1u : 0u);
             umma_commit(&sm->s_full[sb]);
             umma_commit(&sm->empty_k[st]);
             if (j == x.n_tiles - 1) umma_commit(&sm->q_empty[qb]);
@@ -494,32 +550,38 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         } else {
           const int ob = ui & 1;
           const uint32_t d = tmem + C::kColO + ob * C::kPCols;
-          if (!mbar_wait(&sm->o_free[ob], ((ui >> 1) & 1) ^ 1, abort_any, p.wait_ns)) {
+          if (!mbar_wait_call(&sm->o_free[ob], ((ui >> 1) & 1) ^ 1, abort_any, p.wait_ns)) {
             failed = true;
             break;
           }
-          for (int j = 0; j < x.n_tiles; ++j, ++gi) {
-            const int st = gi % NS, bb = gi & 1;
-            if (!mbar_wait(&sm->full_v[st], (gi / NS) & 1, abort_any, p.wait_ns) ||
-                !mbar_wait(&sm->p_full[bb], (gi >> 1) & 1, abort_any, p.wait_ns)) {
+          for (int j = 0; j < x.n_tiles; j += 2, ++pi) {
+            const int bb = pi % C::kNP, nh = min(2, x.n_tiles - j);
+            if (!mbar_wait_call(&sm->p_full[bb], (pi / C::kNP) & 1, abort_any, p.wait_ns)) {
               failed = true;
               break;
             }
-            tc_fence_after_sync();
-            // V^T: MN-major, 32 tokens (four 8-token atoms) per step.  D = 64:
-            // both M halves read the same 64 columns; lanes 64..127 are unused.
-            const uint64_t a = smem_desc(sbase + C::kOffV + st * C::kKVBytes, 0, C::kAtom, C::kLayout);
-            // P^T: MN-major, no swizzle; 16-column groups 128 B apart, 8-token
-            // groups kPKGroup apart
-            const uint64_t b = smem_desc(sbase + C::kOffP + bb * C::kPBytes, C::kPKGroup, 128,
-                                         kLayoutInterleave);
+            for (int h = 0; h < nh && !failed; ++h, ++gi) {
+              const int st = gi % NSV;
+              if (!mbar_wait_call(&sm->full_v[st], (gi / NSV) & 1, abort_any, p.wait_ns)) {
+                failed = true;
+                break;
+              }
+              tc_fence_after_sync();
+              // V^T: MN-major, 32 tokens (four 8-token atoms) per step.  D = 64:
+              // both M halves read the same 64 columns; lanes 64..127 are unused.
+              const uint64_t a = smem_desc(sbase + C::kOffV + st * C::kKVBytes, 0, C::kAtom, C::kLayout);
+              // P^T: MN-major, no swizzle; 16-column groups 128 B apart, 8-token
+              // groups kPKGroup apart
+              const uint64_t b = smem_desc(sbase + C::kOffP + bb * C::kPBytes + h * C::kPTile,
+                                           C::kPKGroup, 128, kLayoutInterleave);
 #pragma unroll
-            for (int kk = 0; kk < kTileTokens / 32; ++kk)
-              umma_f8(d, a + kk * (4 * C::kAtom >> 4), b + kk * (4 * C::kPKGroup >> 4), kPv,
-                      (j == 0 && kk == 0) ? 0u : 1u);
+              for (int kk = 0; kk < kTileTokens / 32; ++kk)
+                umma_f8(d, a + kk * (4 * C::kAtom >> 4), b + kk * (4 * C::kPKGroup >> 4), kPv,
+                        (j == 0 && h == 0 && kk == 0) ? 0u : 1u);
+              umma_commit(&sm->empty_v[st]);
+            }
             umma_commit(&sm->o_full[bb]);
-            umma_commit(&sm->empty_v[st]);
-            if (j == x.n_tiles - 1) umma_commit(&sm->unit_done[ob]);
+            if (j + 2 >= x.n_tiles) umma_commit(&sm->unit_done[ob]);
           }
         }
         ++ui;
@@ -529,21 +591,21 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
       uint64_t *drain = &sm->drain[is_qk ? 0 : 1];
       umma_commit(drain);
       volatile int no_abort = 0;
-      mbar_wait(drain, 0, &no_abort);
+      mbar_wait_call(drain, 0, &no_abort);
     }
-  } else if (warp < kCorrWarp0) {
+  } else if (warp < C::kCorr0) {
     // ------------------------------------------------------------------
-    // Softmax warpgroups: warpgroup wg takes the tiles with gi % 2 == wg;
-    // thread t <-> TMEM lane t <-> token t of the tile.
+    // Softmax warpgroups: warpgroup wg takes the pairs of tiles with pi % kNW
+    // == wg; thread t <-> TMEM lane t <-> token t of either tile.
     // ------------------------------------------------------------------
     const int wg = warp >> 2, wq = warp & 3, t = threadIdx.x & 127;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t bar_id = 1 + wg;
     const float NEG_INF = neg_inf();
-    int gbase = 0, uo = 0;  // uo: ordinal of the unit among this CTA's units with work
+    int gbase = 0, pbase = 0, uo = 0;  // uo: ordinal of the unit among this CTA's units with work
     bool stop = false;
     for (int k = 0; k < sc.count && !stop; ++k) {
-      const Unit x = sc.get<N>(p, k);
+      const Unit x = unit8<N>(p, sc, k);
       if (x.n_tiles == 0) continue;
       const uint32_t ocol = tmem + lane_off + C::kColO + (uo & 1) * C::kPCols;  // this unit's O^T
       if (t < N) {
@@ -558,173 +620,190 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
       }
       // the unit's Q and row factors are staged (the buffer is not filled
       // again before this unit's epilogue, so the phase cannot move on)
-      const bool okq = mbar_wait(&sm->q_full[uo % QB], (uo / QB) & 1, abort_any, p.wait_ns);
+      const bool okq = mbar_wait_call(&sm->q_full[uo % QB], (uo / QB) & 1, abort_any, p.wait_ns);
       const float *rowf = sm->rowf[uo % QB];
       if (wg_bar_or(bar_id, !okq)) {
         stop = true;
         break;
       }
-      for (int j = 0; j < x.n_tiles; ++j) {
-        const int gi = gbase + j;
-        if ((gi & 1) != wg) continue;
-        const int bb = wg, st = gi % NS, sb = gi % C::kSB, par = (gi >> 1) & 1;
-        // V landed: the stage's scale bytes are staged with it (the stage is
-        // not refilled before this tile's P.V)
-        bool ok = mbar_wait(&sm->full_v[st], (gi / NS) & 1, abort_any, p.wait_ns);
-        ok = mbar_wait(&sm->s_full[sb], (gi / C::kSB) & 1, abort_any, p.wait_ns) && ok;
-        // P^T[bb] is free once P.V of tile gi - 2 is done, the row statistics
-        // once the correction of tile gi - 2 has read them
-        ok = mbar_wait(&sm->o_full[bb], par ^ 1, abort_any, p.wait_ns) && ok;
-        ok = mbar_wait(&sm->stat_free[bb], par ^ 1, abort_any, p.wait_ns) && ok;
-        tc_fence_after_sync();
-        float sv[N];
+      for (int j = 0; j < x.n_tiles; j += 2) {
+        const int pi = pbase + (j >> 1);
+        if (pi % C::kNW != wg) continue;
+        const int g0 = gbase + j, bb = pi % C::kNP;
+        const int use = pi / C::kNP;  // of the P^T buffer and the statistics beside it
+        const bool two = j + 1 < x.n_tiles;
+        bool ok = true;
+        constexpr int kLd = 2 * N;  // S_hi and S_lo
+        float sv[2][kLd];
+        float ks[2], ev[2], iv[2];
 #pragma unroll
-        for (int ch = 0; ch < N / 16; ++ch)
-          if (ch * 16 < x.rows)
-            tmem_ld16(tmem + lane_off + sb * N + ch * 16, *reinterpret_cast<float(*)[16]>(&sv[ch * 16]));
-        const int tok0 = x.tok0 + j * kTileTokens;
-        const int tok = tok0 + t;
-        const bool held = tok < x.lim_max;
-        const int kb = held ? sm->sc[st][0][t >> p.box_shift] : 127;
-        const int vb = held ? sm->sc[st][1][t >> p.box_shift] : 127;
-        const float ks = scale_of(kb), ev = static_cast<float>(vb - 127), iv = inv_scale_of(vb);
-#pragma unroll
-        for (int ch = 0; ch < N / 16; ++ch)
-          if (ch * 16 < x.rows) tmem_ld_wait_for(*reinterpret_cast<float(*)[16]>(&sv[ch * 16]));
-        // the S^T buffer is read
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm->s_free[sb]);
-        if (tok0 + kTileTokens > x.lim_max && ok && !held) {
-          // The last tile: keys past the loaded range hold stale bytes; zero
-          // those V rows so that 0 * V stays 0 in P.V.
-          uint4 *vrow = reinterpret_cast<uint4 *>(smem + C::kOffV + st * C::kKVBytes + t * D);
-#pragma unroll
-          for (int k16 = 0; k16 < D / 16; ++k16) vrow[k16] = make_uint4(0u, 0u, 0u, 0u);
-        }
-        float(*wmax)[N] = sm->wmax[wg][par];
-#pragma unroll
-        for (int q4 = 0; q4 < N / 4; ++q4) {
-          if (q4 * 4 < x.rows) {  // warp-uniform: padded rows need no reduction
-            const int4 lim = *reinterpret_cast<const int4 *>(&sm->lim[wg][4 * q4]);
-            const float4 rf = *reinterpret_cast<const float4 *>(&rowf[4 * q4]);
-            const int lims[4] = {lim.x, lim.y, lim.z, lim.w};
-            const float rfs[4] = {rf.x, rf.y, rf.z, rf.w};
-            float v[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int c = 4 * q4 + e;
-              // (masked, and rows past x.rows, whose limit is 0: the score
-              // itself is -inf from here on)
-              const bool seen = tok < lims[e];
-              sv[c] = seen ? sv[c] : NEG_INF;
-              v[e] = seen ? __fmaf_rn(sv[c], __fmul_rn(rfs[e], ks), ev) : NEG_INF;
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = warp_max(v[e]);
-            if (lane == 0)
-              *reinterpret_cast<float4 *>(&wmax[wq][4 * q4]) = make_float4(v[0], v[1], v[2], v[3]);
+        for (int h = 0; h < 2; ++h) {
+          if (h == 0 || two) {
+            const int g = g0 + h, sb = g % C::kSB, sl = g % C::kSC;
+            ok = mbar_wait_call(&sm->sc_full[sl], (g / C::kSC) & 1, abort_any, p.wait_ns) && ok;
+            ok = mbar_wait_call(&sm->s_full[sb], (g / C::kSB) & 1, abort_any, p.wait_ns) && ok;
+            tc_fence_after_sync();
+            tmem_ld_cols<kLd>(tmem + lane_off + sb * C::kQCols, sv[h]);
           }
         }
+        const int tok0 = x.tok0 + j * kTileTokens + t;  // token of the first tile; the second's is 128 on
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int sl = (g0 + h) % C::kSC;
+          const int both = tok0 + h * kTileTokens < x.lim_max ? sm->sc[sl][t >> p.box_shift] : 127 | (127 << 8);
+          ks[h] = scale_of(both & 255);
+          ev[h] = static_cast<float>((both >> 8) - 127);
+          iv[h] = inv_scale_of(both >> 8);
+        }
+        tmem_ld_cols_wait<kLd>(sv[0]);
+        if (two) tmem_ld_cols_wait<kLd>(sv[1]);
+        // the S^T buffers are read
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sm->s_free[g0 % C::kSB]);
+          if (two) mbar_arrive(&sm->s_free[(g0 + 1) % C::kSB]);
+        }
+        if (x.tok0 + (j + 2) * kTileTokens > x.lim_max && j + 2 >= x.n_tiles) {
+          // The unit's last tile: keys past the loaded range hold stale bytes;
+          // once V has landed, zero those V rows so that 0 * V stays 0 in P.V.
+          const int h = two ? 1 : 0, st = (g0 + h) % NSV;
+          ok = mbar_wait_call(&sm->full_v[st], ((g0 + h) / NSV) & 1, abort_any, p.wait_ns) && ok;
+          if (ok && tok0 + h * kTileTokens >= x.lim_max) {
+            uint4 *vrow = reinterpret_cast<uint4 *>(smem + C::kOffV + st * C::kKVBytes + t * D);
+#pragma unroll
+            for (int k16 = 0; k16 < D / 16; ++k16) vrow[k16] = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        float(*wmax)[N] = sm->wmax[wg][(pi / C::kNW) & 1];
+#pragma unroll
+        for (int q4 = 0; q4 < N / 4; ++q4) {
+          const int4 lim = *reinterpret_cast<const int4 *>(&sm->lim[wg][4 * q4]);
+          const float4 rf = *reinterpret_cast<const float4 *>(&rowf[4 * q4]);
+          const int lims[4] = {lim.x, lim.y, lim.z, lim.w};
+          const float rfs[4] = {rf.x, rf.y, rf.z, rf.w};
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int c = 4 * q4 + e;
+            v[e] = NEG_INF;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              // (masked, a missing second tile, and rows past x.rows, whose
+              // limit is 0: the score itself is -inf from here on)
+              const bool seen = (h == 0 || two) && tok0 + h * kTileTokens < lims[e];
+              sv[h][c] = seen ? join_q(sv[h][c], sv[h][N + c]) : NEG_INF;
+              if (seen) v[e] = fmaxf(v[e], __fmaf_rn(sv[h][c], __fmul_rn(rfs[e], ks[h]), ev[h]));
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = warp_max(v[e]);
+          if (lane == 0)
+            *reinterpret_cast<float4 *>(&wmax[wq][4 * q4]) = make_float4(v[0], v[1], v[2], v[3]);
+        }
+        // P^T[bb] is free once P.V of pair pi - kNP is done, the row statistics
+        // once the correction of that pair has read them
+        ok = mbar_wait_call(&sm->o_full[bb], (use & 1) ^ 1, abort_any, p.wait_ns) && ok;
+        ok = mbar_wait_call(&sm->stat_free[bb], (use & 1) ^ 1, abort_any, p.wait_ns) && ok;
         if (wg_bar_or(bar_id, !ok)) {
           stop = true;
           break;
         }
-        // the running references: the previous tile's, this tile's.  Every
+        // the running references: the previous pair's, this pair's.  Every
         // warp works them out for itself (lane = row), so that the chain from
-        // tile to tile has no barrier in it; warp 0 publishes them.
-        if (gi > 0)
-          ok = mbar_wait(&sm->m_full[(gi - 1) & 1], ((gi - 1) >> 1) & 1, abort_any, p.wait_ns) && ok;
+        // pair to pair has no barrier in it; warp 0 publishes them.
+        if (pi > 0)
+          ok = mbar_wait_call(&sm->m_full[(pi - 1) & 1], ((pi - 1) >> 1) & 1, abort_any, p.wait_ns) && ok;
         bool moved = false;
-#pragma unroll
-        for (int c0 = 0; c0 < N; c0 += 32) {
-          const int c = c0 + lane;
-          if (c < N) {
-            float m_new = NEG_INF, a = 1.f;
-            if (c < x.rows) {
-              const float tmax = fmaxf(fmaxf(wmax[0][c], wmax[1][c]), fmaxf(wmax[2][c], wmax[3][c]));
-              const float m_prev = j > 0 ? sm->mrun[(gi - 1) & 1][c] : NEG_INF;
-              m_new = (tmax > __fadd_rn(m_prev, kRefTop)) ? __fsub_rn(tmax, kRefDrop) : m_prev;
-              a = (m_prev == NEG_INF || m_new == m_prev) ? 1.f : ex2(__fsub_rn(m_prev, m_new));
-            }
-            sm->mw[wg][wq][c] = m_new;
-            sm->aw[wg][wq][c] = a;
-            moved = moved || a != 1.f;
-            if (wq == 0) {
-              sm->mrun[gi & 1][c] = m_new;
-              sm->mnew[bb][c] = m_new;
-              sm->scl[bb][c] = a;
-            }
+        if (lane < N) {
+          const int c = lane;
+          float m_new = NEG_INF, a = 1.f;
+          if (c < x.rows) {
+            const float tmax = fmaxf(fmaxf(wmax[0][c], wmax[1][c]), fmaxf(wmax[2][c], wmax[3][c]));
+            const float m_prev = j > 0 ? sm->mrun[(pi - 1) & 1][c] : NEG_INF;
+            m_new = (tmax > __fadd_rn(m_prev, kRefTop)) ? __fsub_rn(tmax, kRefDrop) : m_prev;
+            a = (m_prev == NEG_INF || m_new == m_prev) ? 1.f : ex2(__fsub_rn(m_prev, m_new));
           }
+          sm->mw[wg][wq][c] = m_new;
+          moved = a != 1.f;
+          if (wq == 0) {
+            sm->mrun[pi & 1][c] = m_new;
+            sm->mnew[bb][c] = m_new;
+            sm->scl[bb][c] = a;
+          }
+          sm->aw[wg][wq][c] = a;
         }
-        const bool resc = __any_sync(0xffffffffu, moved);  // (also orders mw / aw for the warp)
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm->m_full[gi & 1]);
+        const bool resc = __any_sync(0xffffffffu, moved);
+        __syncwarp();  // (mw / aw, for the warp)
+        if (lane == 0) mbar_arrive(&sm->m_full[pi & 1]);
         if (resc) {
-          // O^T holds the unit's tiles < gi once P.V(gi - 1) is done (see
-          // attn_split.cuh on the parity)
-          ok = mbar_wait(&sm->o_full[(gi - 1) & 1], ((gi - 1) >> 1) & 1, abort_any, p.wait_ns) && ok;
+          // O^T holds the unit's earlier pairs once P.V of pair pi - 1 is done
+          // (o_full of its buffer: the phase before is pair pi - 1 - kNP's, done
+          // since that of pair pi - kNP was awaited above, and the one after
+          // needs this pair)
+          ok = mbar_wait_call(&sm->o_full[(pi - 1) % C::kNP], ((pi - 1) / C::kNP) & 1, abort_any, p.wait_ns) && ok;
           if (__all_sync(0xffffffffu, ok)) {
             tc_fence_after_sync();
+#pragma unroll 1
+            for (int c0 = 0; c0 < C::kPCols; c0 += 16) {
+              float o[16];
+              tmem_ld16(ocol + c0, o);
+              tmem_ld_wait_for(o);
+              uint32_t w[16];
 #pragma unroll
-            for (int ch = 0; ch < N / 16; ++ch) {
-              if (ch * 16 < x.rows) {  // warp-uniform
-                float hi[16], mid[16];
-                tmem_ld16(ocol + ch * 16, hi);
-                tmem_ld16(ocol + N + ch * 16, mid);
-                tmem_ld_wait_for(hi);
-                tmem_ld_wait_for(mid);
-                uint32_t wh[16], wm[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  const float a = sm->aw[wg][wq][ch * 16 + e];
-                  wh[e] = __float_as_uint(__fmul_rn(hi[e], a));
-                  wm[e] = __float_as_uint(__fmul_rn(mid[e], a));
-                }
-                tmem_st16(ocol + ch * 16, wh);
-                tmem_st16(ocol + N + ch * 16, wm);
-              }
+              for (int e = 0; e < 16; ++e)  // (column c: row c % N; padding columns hold zeros)
+                w[e] = __float_as_uint(__fmul_rn(o[e], sm->aw[wg][wq][(c0 + e) % N]));
+              tmem_st16(ocol + c0, w);
             }
             tmem_st_wait();
           }
         }
-        // P^T row t: one 16-byte chunk of hi and of mid per 16 rows
+        // P^T row t of either tile: bytes [hi | mid | lo] of the rows
         uint8_t *prow = smem + C::kOffP + bb * C::kPBytes + (t >> 3) * C::kPKGroup + (t & 7) * 16;
 #pragma unroll
-        for (int grp = 0; grp < N / 16; ++grp) {
-          uint32_t wh[4], wm[4];
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[C::kPCols / 4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int c0 = grp * 16 + 4 * e;
-            SplitP a{0u, 0u}, b{0u, 0u};
-            if (c0 < x.rows) {  // groups of padded rows keep p = 0
-              const float4 rf = *reinterpret_cast<const float4 *>(&rowf[c0]);
-              const float4 mm = *reinterpret_cast<const float4 *>(&sm->mw[wg][wq][c0]);
-              const float rfs[4] = {rf.x, rf.y, rf.z, rf.w}, ms[4] = {mm.x, mm.y, mm.z, mm.w};
+          for (int i = 3 * N / 4; i < C::kPCols / 4; ++i) w[i] = 0u;
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                sv[c0 + i] = (sv[c0 + i] == NEG_INF)
-                                 ? 0.f
-                                 : ex2(__fmaf_rn(sv[c0 + i], __fmul_rn(rfs[i], ks), __fsub_rn(ev, ms[i])));
-              a = split_p(sv[c0], sv[c0 + 1]);
-              b = split_p(sv[c0 + 2], sv[c0 + 3]);
+          for (int q4 = 0; q4 < N / 4; ++q4) {
+            const float4 rf = *reinterpret_cast<const float4 *>(&rowf[4 * q4]);
+            const float4 mm = *reinterpret_cast<const float4 *>(&sm->mw[wg][wq][4 * q4]);
+            const float rfs[4] = {rf.x, rf.y, rf.z, rf.w}, ms[4] = {mm.x, mm.y, mm.z, mm.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float &s = sv[h][4 * q4 + i];
+              s = (s == NEG_INF) ? 0.f : ex2(__fmaf_rn(s, __fmul_rn(rfs[i], ks[h]), __fsub_rn(ev[h], ms[i])));
             }
-            wh[e] = a.hi | (b.hi << 16);
-            wm[e] = a.mid | (b.mid << 16);
+            const SplitP a = split_p(sv[h][4 * q4], sv[h][4 * q4 + 1]);
+            const SplitP b = split_p(sv[h][4 * q4 + 2], sv[h][4 * q4 + 3]);
+            w[q4] = a.hi | (b.hi << 16);
+            w[N / 4 + q4] = a.mid | (b.mid << 16);
+            w[N / 2 + q4] = a.lo | (b.lo << 16);
           }
-          *reinterpret_cast<uint4 *>(prow + grp * 128) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
-          *reinterpret_cast<uint4 *>(prow + (N / 16 + grp) * 128) = make_uint4(wm[0], wm[1], wm[2], wm[3]);
+#pragma unroll
+          for (int i = 0; i < C::kPCols / 16; ++i)
+            *reinterpret_cast<uint4 *>(prow + h * C::kPTile + i * 128) =
+                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         }
+        // the pair's row sums: p 2^-ev of both tiles, then a tree over the
+        // lanes that halves the rows a lane carries twice (six shuffles for
+        // four rows); lane 8 r holds row r
 #pragma unroll
         for (int q4 = 0; q4 < N / 4; ++q4) {
-          if (q4 * 4 < x.rows) {
-            float v[4];
+          float v[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = __fmul_rn(sv[4 * q4 + e], iv);
-            warp_sum4_lane0(v);
-            if (lane == 0)
-              *reinterpret_cast<float4 *>(&sm->wsum[bb][wq][4 * q4]) = make_float4(v[0], v[1], v[2], v[3]);
-          }
+          for (int e = 0; e < 4; ++e)
+            v[e] = __fmaf_rn(sv[1][4 * q4 + e], iv[1], __fmul_rn(sv[0][4 * q4 + e], iv[0]));
+          const bool up = lane & 16, up2 = lane & 8;
+          float a0 = up ? v[2] : v[0], a1 = up ? v[3] : v[1];
+          a0 = __fadd_rn(a0, __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 16));
+          a1 = __fadd_rn(a1, __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 16));
+          float b = up2 ? a1 : a0;
+          b = __fadd_rn(b, __shfl_xor_sync(0xffffffffu, up2 ? a0 : a1, 8));
+#pragma unroll
+          for (int off = 4; off >= 1; off >>= 1) b = __fadd_rn(b, __shfl_xor_sync(0xffffffffu, b, off));
+          if ((lane & 7) == 0) sm->wsum[bb][wq][4 * q4 + (lane >> 3)] = b;
         }
         fence_proxy_async_smem();
         tc_fence_before_sync();
@@ -732,25 +811,26 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         if (lane == 0) mbar_arrive(&sm->p_full[bb]);
       }
       gbase += x.n_tiles;
+      pbase += (x.n_tiles + 1) >> 1;
       ++uo;
     }
     (void)stop;
-  } else if (warp < kCorrWarp0 + 4) {
+  } else if (warp < C::kPrepW) {
     // ------------------------------------------------------------------
     // Correction + epilogue warpgroup: thread r (< rows) owns row r's
     // running l; at the unit's end thread t <-> column d of O^T.
     // ------------------------------------------------------------------
     const int wq = warp & 3, t = threadIdx.x & 127;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
-    constexpr uint32_t bar_id = 3;
+    constexpr uint32_t bar_id = 1 + C::kNW;
     const float NEG_INF = neg_inf();
     float acc[N];
     float m_run = NEG_INF, l_run = 0.f;
-    int gbase = 0, cui = 0;
+    int pbase = 0, cui = 0;
     bool bulk_out = false;   // thread 0 has bulk stores to complete before exit
     bool stop = false;
     for (int k = 0; k < sc.count && !stop; ++k) {
-      const Unit x = sc.get<N>(p, k);
+      const Unit x = unit8<N>(p, sc, k);
       if (t == 0) check_sequence(p, x);
       if (x.n_tiles == 0) {
         // direct write: rows of this unit see no key (out = 0, lse = -inf)
@@ -766,9 +846,9 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
       }
       m_run = NEG_INF;
       l_run = 0.f;
-      for (int j = 0; j < x.n_tiles; ++j) {
-        const int gi = gbase + j, bb = gi & 1, par = (gi >> 1) & 1;
-        const bool ok = mbar_wait(&sm->p_full[bb], par, abort_any, p.wait_ns);  // the tile's row statistics
+      for (int j = 0; j < (x.n_tiles + 1) >> 1; ++j) {
+        const int pi = pbase + j, bb = pi % C::kNP;
+        const bool ok = mbar_wait_call(&sm->p_full[bb], (pi / C::kNP) & 1, abort_any, p.wait_ns);  // the pair's row statistics
         if (t < x.rows) {
           const float lt = __fadd_rn(__fadd_rn(sm->wsum[bb][0][t], sm->wsum[bb][1][t]),
                                      __fadd_rn(sm->wsum[bb][2][t], sm->wsum[bb][3][t]));
@@ -776,7 +856,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
           m_run = sm->mnew[bb][t];
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm->stat_free[bb]);  // the tile's statistics are read
+        if (lane == 0) mbar_arrive(&sm->stat_free[bb]);  // the pair's statistics are read
         if (wg_bar_or(bar_id, !ok)) {
           stop = true;
           break;
@@ -785,24 +865,24 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
       if (stop) break;
       {
         const int ob = cui & 1;
-        const bool ok = mbar_wait(&sm->unit_done[ob], (cui >> 1) & 1, abort_any, p.wait_ns);
+        const bool ok = mbar_wait_call(&sm->unit_done[ob], (cui >> 1) & 1, abort_any, p.wait_ns);
         if (wg_bar_or(bar_id, !ok)) {
           stop = true;
           break;
         }
         tc_fence_after_sync();
+        float o[3 * N];
+        tmem_ld_cols<3 * N / 8 * 8>(tmem + lane_off + C::kColO + ob * C::kPCols, o);
+        if constexpr (3 * N % 8 != 0) {
+          float last[8];
+          tmem_ld8(tmem + lane_off + C::kColO + ob * C::kPCols + 3 * N / 8 * 8, last);
+          tmem_ld_wait_for8(last);
 #pragma unroll
-        for (int ch = 0; ch < N / 16; ++ch) {
-          if (ch * 16 < x.rows) {  // warp-uniform
-            float hi[16], mid[16];
-            tmem_ld16(tmem + lane_off + C::kColO + ob * C::kPCols + ch * 16, hi);
-            tmem_ld16(tmem + lane_off + C::kColO + ob * C::kPCols + N + ch * 16, mid);
-            tmem_ld_wait_for(hi);
-            tmem_ld_wait_for(mid);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) acc[ch * 16 + e] = __fmaf_rn(mid[e], kMidScale, hi[e]);
-          }
+          for (int e = 3 * N / 8 * 8; e < 3 * N; ++e) o[e] = last[e % 8];
         }
+        tmem_ld_cols_wait<3 * N / 8 * 8>(o);
+#pragma unroll
+        for (int c = 0; c < N; ++c) acc[c] = join_p(o[c], o[N + c], o[2 * N + c]);
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm->o_free[ob]);
@@ -873,7 +953,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         mbar_arrive(&sm->q_empty[cui % QB]);
       }
       ++cui;
-      gbase += x.n_tiles;
+      pbase += (x.n_tiles + 1) >> 1;
     }
     // the partials are complete in global memory before the CTA leaves
     if (bulk_out) bulk_wait<0>();
@@ -882,7 +962,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
 
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == C::kQkW) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, C::kTmemCols);
   }

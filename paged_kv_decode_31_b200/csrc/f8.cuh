@@ -27,11 +27,6 @@ __device__ __forceinline__ uint32_t e4m3x2_of(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ uint32_t e5m2x2_of(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 __device__ __forceinline__ uint32_t e4m3x2_of(__half2 v) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<uint32_t *>(&v)));
@@ -43,13 +38,12 @@ __device__ __forceinline__ __half2 half2_of_e4m3x2(uint32_t v) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(v)));
   return *reinterpret_cast<__half2 *>(&r);
 }
-// A query row enters K Q^T as two 8-bit operands of one scale: the row times
-// 2^k, k chosen so that its largest magnitude lies in [128, 256), is
-// hi + lo with hi = e4m3(x) and lo = e5m2(x - hi).  A bf16 value has 8
-// significant bits, hi takes the first 4 and the remainder (at most 8 units of
-// the last bit) needs 3, which e5m2 has: the sum is exact for every element
-// down to 2^-13 of the row's largest, and within 2^-21 of that largest below
-// (where hi is subnormal).
+// A query row enters K Q^T as two e4m3 operands whose products are accumulated
+// apart and joined in fp32 as hi + lo / 16: the row times 2^k, k chosen so that
+// its largest magnitude lies in [128, 256), is taken apart as hi = e4m3(x) and
+// lo = e4m3(16 (x - hi)).  A bf16 value has 8 significant bits, hi takes the
+// first 4 and lo holds the rest: exact for every element down to 2^-13 of the
+// row's largest, and within 2^-21 of that largest below.
 struct Split2 {
   uint32_t hi, lo;  // two elements each, packed
 };
@@ -57,27 +51,34 @@ __device__ __forceinline__ Split2 split_q(float x0, float x1) {
   Split2 s;
   s.hi = e4m3x2_of(x0, x1);
   const float2 h = __half22float2(half2_of_e4m3x2(s.hi));
-  s.lo = e5m2x2_of(__fsub_rn(x0, h.x), __fsub_rn(x1, h.y));
+  s.lo = e4m3x2_of(__fmul_rn(__fsub_rn(x0, h.x), 16.f), __fmul_rn(__fsub_rn(x1, h.y), 16.f));
   return s;
 }
+__device__ __forceinline__ float join_q(float hi, float lo) { return __fmaf_rn(lo, 0.0625f, hi); }
 
-// A probability in [0, 256] enters P V as two e4m3 operands, hi = e4m3(p) and
-// mid = e4m3(16 (p - hi)), whose products are accumulated apart and joined as
-// hi + mid / 16 in fp32.  hi leaves at most 2^-4 of p's power of two, mid keeps
-// 4 bits of that: p is off by at most 2^-9 relative (5.9e-4 rms), half of what
-// rounding P to bf16 would do and a quarter of a bf16 output's own half step;
-// below 2^-6 by at most 2^-14, half of mid's smallest step.  (The differences
-// are taken from p rounded to fp16, 2^-11, which is below all of that.)
+// A probability in [0, 256], rounded to fp16 (11 bits: off by at most 2^-11
+// relative), enters P V as three e4m3 operands whose products are accumulated
+// apart and joined in fp32 as hi + (mid + lo / 16) / 16:
+//   hi = e4m3(p),  mid = e4m3(16 (p - hi)),  lo = e4m3(16 (16 (p - hi) - mid)).
+// The differences are exact in fp16, and hi and mid leave at most two units of
+// p's last bit to lo, so the three hold the fp16 value; small ones too, down
+// to half of lo's smallest step, 2^-18.
 struct SplitP {
-  uint32_t hi, mid;
+  uint32_t hi, mid, lo;
 };
 __device__ __forceinline__ SplitP split_p(float p0, float p1) {
   SplitP s;
-  const __half2 r = __floats2half2_rn(p0, p1);
+  const __half2 k16 = __floats2half2_rn(16.f, 16.f);
+  __half2 r = __floats2half2_rn(p0, p1);
   s.hi = e4m3x2_of(r);
-  s.mid = e4m3x2_of(__hmul2(__hsub2(r, half2_of_e4m3x2(s.hi)), __floats2half2_rn(16.f, 16.f)));
+  r = __hmul2(__hsub2(r, half2_of_e4m3x2(s.hi)), k16);
+  s.mid = e4m3x2_of(r);
+  r = __hmul2(__hsub2(r, half2_of_e4m3x2(s.mid)), k16);
+  s.lo = e4m3x2_of(r);
   return s;
 }
-constexpr float kMidScale = 0.0625f;
+__device__ __forceinline__ float join_p(float hi, float mid, float lo) {
+  return __fmaf_rn(__fmaf_rn(lo, 0.0625f, mid), 0.0625f, hi);
+}
 
 }  // namespace pkv

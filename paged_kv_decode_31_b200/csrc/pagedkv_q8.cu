@@ -55,21 +55,25 @@ bool strides16_ok(const int64_t *st) {
   return true;
 }
 
-// K/V stages: as many as the 227 KB of shared memory hold beside Q and P (the
-// bytes in flight per SM are those of the bf16 kernel's 192 KB).
-template <int D, int N>
-constexpr int stages_q8() {
-  return (D == 128 ? 1 : 2) * (N == 16 ? 6 : 4);
+// K and V stages.  A K tile is done with once its S^T is computed, a V tile is
+// held until its P.V, 2700 cycles of softmax later.
+template <int D>
+constexpr int k_stages() {
+  return D == 128 ? 4 : 8;
+}
+template <int D>
+constexpr int v_stages() {
+  return D == 128 ? 6 : 10;
 }
 
 template <int D, int N>
 int launch_split_q8(const Q8Params &p, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t s,
                     int dev) {
-  constexpr int NS = stages_q8<D, N>();
-  using C = Q8Cfg<D, N, NS>;
+  constexpr int NSK = k_stages<D>(), NSV = v_stages<D>();
+  using C = Q8Cfg<D, N, NSK, NSV>;
   static_assert(C::kSmemBytes <= 232448, "shared memory budget");
   static std::atomic<bool> attr_set[kMaxDevices];
-  auto kern = attn_split_q8_kernel<D, N, NS>;
+  auto kern = attn_split_q8_kernel<D, N, NSK, NSV>;
   if (dev < 0 || dev >= kMaxDevices || !attr_set[dev].load(std::memory_order_acquire)) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) !=
         cudaSuccess)
@@ -79,7 +83,7 @@ int launch_split_q8(const Q8Params &p, const CUtensorMap &mk, const CUtensorMap 
   const int grid = p.n_units < sm_count(dev) ? p.n_units : sm_count(dev);
   Q8Params pp = p;
   pp.sched = p.n_units <= C::kSchedScratch ? 1 : 0;
-  kern<<<grid, kQ8Threads, C::kSmemBytes, s>>>(pp, mk, mv);
+  kern<<<grid, 32 * C::kWarps, C::kSmemBytes, s>>>(pp, mk, mv);
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
@@ -123,7 +127,7 @@ int attn_q8_entry(const void *q, const int64_t q_strides[3], const void *k_cache
   const int64_t tokens = pq ? static_cast<int64_t>(pq->total_q) : static_cast<int64_t>(batch) * seqlen_q;
   const int64_t rows = tokens * Hq;
   if (R > INT32_MAX / 2 || rows > INT32_MAX) return PKV_ERR_ARG;
-  const int N = R <= 16 ? 16 : 64;
+  const int N = R <= 4 ? 4 : R <= 8 ? 8 : 16;
   const int64_t S = max_seqlen_k > 0 ? ceil_div(max_seqlen_k, kSplitTokens) : 1;
   const int64_t RT = ceil_div(R, N);
   const int64_t units = static_cast<int64_t>(batch) * S * Hkv * RT;
@@ -204,9 +208,13 @@ int attn_q8_entry(const void *q, const int64_t q_strides[3], const void *k_cache
                   : 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (D == 128)
-    rc = N == 16 ? launch_split_q8<128, 16>(p, mk, mv, s, dev) : launch_split_q8<128, 64>(p, mk, mv, s, dev);
+    rc = N == 4   ? launch_split_q8<128, 4>(p, mk, mv, s, dev)
+         : N == 8 ? launch_split_q8<128, 8>(p, mk, mv, s, dev)
+                  : launch_split_q8<128, 16>(p, mk, mv, s, dev);
   else
-    rc = N == 16 ? launch_split_q8<64, 16>(p, mk, mv, s, dev) : launch_split_q8<64, 64>(p, mk, mv, s, dev);
+    rc = N == 4   ? launch_split_q8<64, 4>(p, mk, mv, s, dev)
+         : N == 8 ? launch_split_q8<64, 8>(p, mk, mv, s, dev)
+                  : launch_split_q8<64, 16>(p, mk, mv, s, dev);
   if (rc != PKV_OK || p.direct) return rc;
 
   MergeParams m{};

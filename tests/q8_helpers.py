@@ -72,12 +72,11 @@ def append_q8(k_new, v_new, kc, vc, ks, vs, table, seqlens, bs):
 def attention(q, kc, vc, ks, vs, table, seqlens, scale, causal, nq=None):
     """fp64 attention of dense q [B, sq, Hq, D] over an 8-bit cache; returns
     out, lse [B, Hq, sq] and the part of out's bound that P's rounding gives:
-    2^-9 + 2^-10 of A = sum p |v| / sum p (two e4m3 operands: hi leaves 2^-4 of
-    p's power of two, mid half a step of that, 2^-9; fp16 before them 2^-11;
-    as much for fp32 noise), and the step that small probabilities keep.  That
-    is 2^-14 (half of mid's smallest step) where the largest p of a row, with
-    its token's V scale 2^ev folded in, is at least 2^6: 2^-20 2^ev |v8| of the
-    result per token, ev at most the largest.
+    2^-10 of A = sum p |v| / sum p (fp16's 2^-11, and as much for fp32 noise),
+    and the step that small probabilities keep.  That is 2^-18 (half of the
+    smallest step of the third operand, 2^-9 / 2^8) where the largest p of a
+    row, with its token's V scale 2^ev folded in, is at least 2^2: 2^-20 2^ev
+    |v8| of the result per token, ev at most the largest.
     nq: the query counts of a padded batch."""
     B, sq, Hq, D = q.shape
     bs, Hkv = kc.shape[1], kc.shape[2]
@@ -103,7 +102,7 @@ def attention(q, kc, vc, ks, vs, table, seqlens, scale, causal, nq=None):
         w = torch.where(torch.isneginf(l)[..., None], 0.0, w)
         lse[b, :, :n] = l
         out[b, :n] = torch.einsum("hij,jhd->ihd", w, v)
-        mag[b, :n] = (2.0 ** -9 + 2.0 ** -10) * torch.einsum("hij,jhd->ihd", w, v.abs())
+        mag[b, :n] = 2.0 ** -10 * torch.einsum("hij,jhd->ihd", w, v.abs())
         mag[b, :n] += tail.repeat_interleave(Hq // Hkv, 0)
     return out, lse, mag
 
