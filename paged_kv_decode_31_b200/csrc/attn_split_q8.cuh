@@ -217,6 +217,21 @@ __device__ __forceinline__ int swz16(int r, int c) {
   return r * D + ((D == 128 ? (c ^ (r & 7)) : (c ^ ((r >> 1) & 3))) << 4);
 }
 
+// The power of two that a query row is multiplied by, and its inverse, from the
+// bits of the row's largest magnitude (ordered like the values, NaN and inf on
+// top): that magnitude goes to [128, 256), exponent field + k = 127 + 7, with k
+// held to [-60, 60] so that c 2^-k 2^ek stays a normal number (rows below 2^-53
+// keep fewer bits, values past 2^68 saturate).  A row with an infinity or NaN
+// is multiplied by 0: those elements become NaN, the rest zero.
+struct QScale {
+  float f, back;
+};
+__device__ __forceinline__ QScale q_scale(uint32_t top) {
+  const bool finite = top < 0x7F80u;
+  const int k = !finite || top == 0 ? 0 : max(-60, min(60, 134 - max(static_cast<int>(top >> 7), 1)));
+  return QScale{finite ? __int_as_float((127 + k) << 23) : 0.f, __int_as_float((127 - k) << 23)};
+}
+
 // The query rows of unit x as q_hi and q_lo (the B operands of S^T) and their
 // factors c 2^-k.  D / 8 lanes share a row, eight elements each; a pass of the
 // warp takes 256 / D rows.  Rows past x.rows keep whatever the buffer holds:
@@ -241,14 +256,8 @@ __device__ __forceinline__ void put_q_pass(const Q8Params &p, uint4 v, int c, ui
 #pragma unroll
   for (int off = kLanes / 2; off >= 1; off >>= 1)
     top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-  const bool finite = top < 0x7F80u;
-  // largest magnitude to [128, 256): exponent field + k = 127 + 7; held to
-  // [-60, 60] so that c 2^-k 2^ek stays a normal number (rows below 2^-53
-  // keep fewer bits, values past 2^68 saturate)
-  int k = 134 - max(static_cast<int>(top >> 7), 1);
-  k = !finite || top == 0 ? 0 : max(-60, min(60, k));
-  // a row with an infinity or NaN: those elements become NaN, the rest zero
-  const float f = finite ? __int_as_float((127 + k) << 23) : 0.f;
+  const QScale qs = q_scale(top);
+  const float f = qs.f;
   uint32_t hi[4], lo[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -261,7 +270,7 @@ __device__ __forceinline__ void put_q_pass(const Q8Params &p, uint4 v, int c, ui
       make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
   *reinterpret_cast<uint2 *>(qdst + swz16<D>(N + c, ch >> 1) + (ch & 1) * 8) =
       make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-  if (ch == 0) rowf[c] = __fmul_rn(p.cscale, __int_as_float((127 - k) << 23));
+  if (ch == 0) rowf[c] = __fmul_rn(p.cscale, qs.back);
 }
 
 // The units of this CTA: from shared memory, where they were worked out once
@@ -352,11 +361,11 @@ __device__ __forceinline__ void prepare_q8(const Q8Params &p, uint8_t *smem, typ
 }
 
 // One loading warp: K (with the tiles' scale bytes) or V of the tiles that go
-// to its stages -- even or odd ones: a stage has one warp, which then waits for
+// to its stages -- even or odd ones, or (kParts = 1) all: a stage has one warp, which then waits for
 // every use of it in turn (a parity wait cannot tell a use from the one two
 // before it).  Eight lanes (boxes) of a tile at once.  The bounded waits and
 // the exit are those of attn_split.cuh's produce().
-template <class C, int NS>
+template <class C, int NS, int kParts>
 __device__ __forceinline__ void load_q8(const Q8Params &p, const CUtensorMap *map, uint8_t *smem,
                                         typename C::Small *sm, uint64_t *full, uint64_t *empty,
                                         uint32_t dst_off, bool is_k, int part, int lane,
@@ -377,7 +386,7 @@ __device__ __forceinline__ void load_q8(const Q8Params &p, const CUtensorMap *ma
     const uint16_t *sct = sm->sctab[ui % US];
     for (int j = 0; j < x.n_tiles; ++j, ++gi) {
       const int st = gi % NS;
-      if ((st & 1) != part) continue;
+      if (kParts == 2 && (st & 1) != part) continue;
       bool okw = true;
       if (lane == 0) okw = mbar_wait_call(&empty[st], ((gi / NS) & 1) ^ 1, abort_any, p.wait_ns);
       if (!__shfl_sync(0xffffffffu, okw ? 1 : 0, 0)) {
@@ -422,7 +431,7 @@ __device__ __forceinline__ void load_q8(const Q8Params &p, const CUtensorMap *ma
     // last tile of each of its stages
     volatile int no_abort = 0;
     for (int g = max(gi - NS, 0); g < gi; ++g)
-      if ((g % NS & 1) == part) mbar_wait_call(&full[g % NS], (g / NS) & 1, &no_abort);
+      if (kParts == 1 || (g % NS & 1) == part) mbar_wait_call(&full[g % NS], (g / NS) & 1, &no_abort);
   }
 }
 
@@ -502,9 +511,9 @@ __global__ void __launch_bounds__(32 * Q8Cfg<D, N, NSK, NSV>::kWarps, 1)
   } else if (warp >= C::kLoadW && warp < C::kQkW) {
     const int w = warp - C::kLoadW;
     if (w < 2)
-      load_q8<C, NSK>(p, &map_k, smem, sm, sm->full_k, sm->empty_k, C::kOffK, true, w, lane, abort_any, sc);
+      load_q8<C, NSK, 2>(p, &map_k, smem, sm, sm->full_k, sm->empty_k, C::kOffK, true, w, lane, abort_any, sc);
     else
-      load_q8<C, NSV>(p, &map_v, smem, sm, sm->full_v, sm->empty_v, C::kOffV, false, w - 2, lane,
+      load_q8<C, NSV, 2>(p, &map_v, smem, sm, sm->full_v, sm->empty_v, C::kOffV, false, w - 2, lane,
                       abort_any, sc);
   } else if (warp == C::kQkW || warp == C::kPvW) {
     // ------------------------------------------------------------------

@@ -56,6 +56,21 @@ __device__ __forceinline__ Split2 split_q(float x0, float x1) {
 }
 __device__ __forceinline__ float join_q(float hi, float lo) { return __fmaf_rn(lo, 0.0625f, hi); }
 
+// The form with one scale, for two products into one accumulator: lo = e5m2(x -
+// hi), whose 3 bits hold the at most 8 units that hi leaves of a bf16 value.
+__device__ __forceinline__ uint32_t e5m2x2_of(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ Split2 split_q_one_scale(float x0, float x1) {
+  Split2 s;
+  s.hi = e4m3x2_of(x0, x1);
+  const float2 h = __half22float2(half2_of_e4m3x2(s.hi));
+  s.lo = e5m2x2_of(__fsub_rn(x0, h.x), __fsub_rn(x1, h.y));
+  return s;
+}
+
 // A probability in [0, 256], rounded to fp16 (11 bits: off by at most 2^-11
 // relative), enters P V as three e4m3 operands whose products are accumulated
 // apart and joined in fp32 as hi + (mid + lo / 16) / 16:

@@ -8,6 +8,7 @@
 #include <cstring>
 
 #include "pagedkv.h"
+#include "attn_rows_q8.cuh"
 #include "attn_split_q8.cuh"
 #include "host.cuh"
 
@@ -87,6 +88,47 @@ int launch_split_q8(const Q8Params &p, const CUtensorMap &mk, const CUtensorMap 
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
+// Decode-sized rows: the smallest unit that holds them.
+int launch_split_q8_rows(int64_t rows, const Q8Params &p, const CUtensorMap &mk, const CUtensorMap &mv,
+                         int D, cudaStream_t s, int dev) {
+  if (D == 128)
+    return rows <= 4   ? launch_split_q8<128, 4>(p, mk, mv, s, dev)
+           : rows <= 8 ? launch_split_q8<128, 8>(p, mk, mv, s, dev)
+                       : launch_split_q8<128, 16>(p, mk, mv, s, dev);
+  return rows <= 4   ? launch_split_q8<64, 4>(p, mk, mv, s, dev)
+         : rows <= 8 ? launch_split_q8<64, 8>(p, mk, mv, s, dev)
+                     : launch_split_q8<64, 16>(p, mk, mv, s, dev);
+}
+
+// The row-major kernel shares out its registers between warpgroups; the
+// launch is refused if the build differs from what the shares add up to.
+template <int D>
+int launch_rows_q8(const Q8Params &p, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t s, int dev) {
+  using C = R8Cfg<D>;
+  static_assert(C::kSmemBytes <= 232448, "shared memory budget");
+  static std::atomic<bool> attr_set[kMaxDevices];
+  auto kern = attn_rows_q8_kernel<D>;
+  if (dev < 0 || dev >= kMaxDevices || !attr_set[dev].load(std::memory_order_acquire)) {
+    cudaFuncAttributes fa{};
+    if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return PKV_ERR_CUDA;
+    if (fa.numRegs != kR8LaunchRegs) return PKV_ERR_CUDA;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) !=
+        cudaSuccess)
+      return PKV_ERR_CUDA;
+    if (dev >= 0 && dev < kMaxDevices) attr_set[dev].store(true, std::memory_order_release);
+  }
+  const int grid = p.n_units < sm_count(dev) ? p.n_units : sm_count(dev);
+  Q8Params pp = p;
+  pp.sched = p.n_units <= C::kSchedScratch ? 1 : 0;
+  kern<<<grid, kR8Threads, C::kSmemBytes, s>>>(pp, mk, mv);
+  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+// Rows per KV head up to which a request is served by the split kernel (one
+// unit of its largest size); its own row count decides, so a row's bits do not
+// depend on the requests beside it.
+constexpr int kSplitRows = 16;
+
 struct PackedQ8 {
   const int32_t *cu_q;
   int total_q;
@@ -127,7 +169,8 @@ int attn_q8_entry(const void *q, const int64_t q_strides[3], const void *k_cache
   const int64_t tokens = pq ? static_cast<int64_t>(pq->total_q) : static_cast<int64_t>(batch) * seqlen_q;
   const int64_t rows = tokens * Hq;
   if (R > INT32_MAX / 2 || rows > INT32_MAX) return PKV_ERR_ARG;
-  const int N = R <= 4 ? 4 : R <= 8 ? 8 : 16;
+  const bool split_only = R <= kSplitRows;
+  const int N = split_only ? (R <= 4 ? 4 : R <= 8 ? 8 : 16) : kRowsPerTile;
   const int64_t S = max_seqlen_k > 0 ? ceil_div(max_seqlen_k, kSplitTokens) : 1;
   const int64_t RT = ceil_div(R, N);
   const int64_t units = static_cast<int64_t>(batch) * S * Hkv * RT;
@@ -207,14 +250,23 @@ int attn_q8_entry(const void *q, const int64_t q_strides[3], const void *k_cache
                   ? 1
                   : 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (D == 128)
-    rc = N == 4   ? launch_split_q8<128, 4>(p, mk, mv, s, dev)
-         : N == 8 ? launch_split_q8<128, 8>(p, mk, mv, s, dev)
-                  : launch_split_q8<128, 16>(p, mk, mv, s, dev);
-  else
-    rc = N == 4   ? launch_split_q8<64, 4>(p, mk, mv, s, dev)
-         : N == 8 ? launch_split_q8<64, 8>(p, mk, mv, s, dev)
-                  : launch_split_q8<64, 16>(p, mk, mv, s, dev);
+  // In a packed call that needs the row-major kernel the short requests take
+  // the split kernel, each launch skipping the other's sequences.
+  const int small_nq = G <= kSplitRows ? kSplitRows / G : 0;
+  const bool both = pq && !split_only && small_nq > 0;
+  if (both) {
+    Q8Params ps = p;
+    ps.nq_lo = 1;
+    ps.nq_hi = small_nq;
+    ps.n_row_tiles = 1;
+    ps.n_units = static_cast<int>(static_cast<int64_t>(batch) * S * Hkv);
+    rc = launch_split_q8_rows(static_cast<int64_t>(small_nq) * G, ps, mk, mv, D, s, dev);
+    if (rc != PKV_OK) return rc;
+    p.nq_lo = small_nq + 1;
+  }
+  rc = split_only ? launch_split_q8_rows(R, p, mk, mv, D, s, dev)
+       : D == 128 ? launch_rows_q8<128>(p, mk, mv, s, dev)
+                  : launch_rows_q8<64>(p, mk, mv, s, dev);
   if (rc != PKV_OK || p.direct) return rc;
 
   MergeParams m{};
@@ -238,6 +290,8 @@ int attn_q8_entry(const void *q, const int64_t q_strides[3], const void *k_cache
   m.fo_sh = p.fo_sh;
   m.fin_lse = p.fin_lse;
   m.rows = rows;
+  m.skip_single = split_only ? 0 : 1;
+  m.skip_min_nq = both ? small_nq + 1 : 0;
   m.n_local = static_cast<int>(S);
   return D == 128 ? launch_merge<128>(m, rows, s) : launch_merge<64>(m, rows, s);
 }

@@ -20,6 +20,7 @@
 
 #include "contract.cuh"
 #include "packed.cuh"
+#include "ptx.cuh"
 
 namespace pkv {
 
@@ -89,8 +90,6 @@ __device__ __forceinline__ int2 piece_chunks(const RopeFreq &f, int u) {
   return make_int2(2 * u, 2 * u + 1);  // (past r the chunks 2u, 2u + 1 are the copied ones)
 }
 
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 __device__ __forceinline__ uint32_t bf2_of(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t *>(&v);
