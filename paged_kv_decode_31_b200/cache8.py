@@ -9,6 +9,7 @@ too).  Argument marshalling only, as in binding.py.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import Optional
 
@@ -16,7 +17,7 @@ import torch
 
 from .binding import (_I, _I64, _P, _check, _need_cache_and_table, _need_cuda_bf16, _need_cuda_i32,
                       _need_err, _need_lse, _need_one_device, _need_packed_bf16, _need_rows, _ptr,
-                      _st2, _st3, lib, varlen_workspace_size, workspace_size)
+                      _st2, lib, varlen_workspace_size, workspace_size)
 from .rotary import _need_freq, _new_tokens, _on, _params, _strides
 
 DEVERR_SCALE = 32
@@ -36,10 +37,14 @@ def _need_cache8(k_cache, v_cache, k_scale, v_scale) -> None:
                              f"[{k_cache.shape[0]}, {k_cache.shape[2]}] (got {list(t.shape)})")
 
 
+@functools.lru_cache(maxsize=4096)
+def _scale_strides(strides: tuple, shape: tuple) -> ctypes.Array:
+    return (ctypes.c_int64 * 2)(*[s if n > 1 else max(s, 1) for s, n in zip(strides, shape)])
+
+
 def _sst(t: torch.Tensor) -> ctypes.Array:
     """(block, head) strides; an axis of size 1 is never stepped over."""
-    return (ctypes.c_int64 * 2)(*[int(s) if n > 1 else max(int(s), 1)
-                                  for s, n in zip(t.stride(), t.shape)])
+    return _scale_strides(t.stride(), t.shape)
 
 
 def kv_append_q8(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor,
@@ -66,8 +71,7 @@ def kv_append_q8(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor
         raise ValueError("q is rotated: it needs inv_freq")
     _need_one_device(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, seqlens, q,
                      inv_freq, cu_seqlens_new, q_out, err)
-    L = lib()
-    fn = L.pkv_kv_append_q8
+    fn = lib().pkv_kv_append_q8
     if not fn.argtypes:
         fn.argtypes = [_P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P,
                        _I64, _P, _I64, _I, _P, _I, _I, _I, _I, _I, _P, _P, _P]
@@ -120,11 +124,11 @@ def _attn_q8(name, q, k_cache, v_cache, k_scale, v_scale, block_table, seqlens, 
                                     device=q.device)
         _need_one_device(q, k_cache, v_cache, k_scale, v_scale, block_table, seqlens, out, lse,
                          workspace, err)
-        rc = fn(q.data_ptr(), _st3(q), k_cache.data_ptr(), _st3(k_cache), v_cache.data_ptr(),
-                _st3(v_cache), k_scale.data_ptr(), _sst(k_scale), v_scale.data_ptr(),
+        rc = fn(q.data_ptr(), _strides(q), k_cache.data_ptr(), _strides(k_cache), v_cache.data_ptr(),
+                _strides(v_cache), k_scale.data_ptr(), _sst(k_scale), v_scale.data_ptr(),
                 _sst(v_scale), num_blocks, block_table.data_ptr(), int(block_table.stride(0)),
                 int(block_table.shape[1]), seqlens.data_ptr(), int(max_seqlen_k), B, sq, Hq, Hkv,
-                D, bs, float(scale), int(bool(causal)), out.data_ptr(), _st3(out), lse.data_ptr(),
+                D, bs, float(scale), int(bool(causal)), out.data_ptr(), _strides(out), lse.data_ptr(),
                 workspace.data_ptr(), workspace.numel() * workspace.element_size(), _ptr(err), s)
         _check(name, rc)
     return out, lse
@@ -196,7 +200,7 @@ def paged_varlen_attn_q8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq
         _need_one_device(q, k_cache, v_cache, k_scale, v_scale, block_table, seqlens, cu_seqlens_q,
                          out, lse, final_out, final_lse, workspace, err)
         rc = fn(q.data_ptr(), _st2(q), cu_seqlens_q.data_ptr(), total_q, int(max_seqlen_q),
-                k_cache.data_ptr(), _st3(k_cache), v_cache.data_ptr(), _st3(v_cache),
+                k_cache.data_ptr(), _strides(k_cache), v_cache.data_ptr(), _strides(v_cache),
                 k_scale.data_ptr(), _sst(k_scale), v_scale.data_ptr(), _sst(v_scale), num_blocks,
                 block_table.data_ptr(), int(block_table.stride(0)), int(block_table.shape[1]),
                 seqlens.data_ptr(), int(max_seqlen_k), B, Hq, Hkv, D, bs, float(scale),

@@ -43,17 +43,19 @@ bool rope_rows(RopeRows *x, const void *src, const int64_t *s, void *dst, const 
   return true;
 }
 
-// Tokens per block of threads: one while that leaves the blocks within a few
-// per SM (latency), then several, so that the position look-ups and the sines
-// of one token hide behind the rows of another.
-int rope_per_block(int64_t tokens, int dev) { return tokens <= 16 * static_cast<int64_t>(sm_count(dev)) ? 1 : 4; }
+// Warps per token, each with at most kRopePasses passes of its rows, evenly.
+void rope_chunks(RopeParams *p) {
+  const int rows = p->x[0].heads + p->x[1].heads + p->x[2].heads, per_pass = 32 / (p->D / 16);
+  p->chunks = static_cast<int>(ceil_div(rows, kRopePasses * per_pass));
+  p->passes = static_cast<int>(ceil_div(ceil_div(rows, p->chunks), per_pass));
+}
 
 int launch_rope(RopeParams &p, cudaStream_t s) {
   if (p.tokens == 0) return PKV_OK;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
-  p.per_block = rope_per_block(p.tokens, dev);
-  rope_kernel<<<static_cast<unsigned>(ceil_div(p.tokens, p.per_block)), kRopeThreads, 0, s>>>(p);
+  rope_chunks(&p);
+  const int64_t blocks = ceil_div(p.tokens * p.chunks, kRopeWarps);
+  if (blocks > INT32_MAX) return PKV_ERR_ARG;
+  rope_kernel<<<static_cast<unsigned>(blocks), kRopeThreads, 0, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
@@ -186,15 +188,39 @@ int pkv_kv_append_q8(const void *q, const int64_t q_strides[3], void *q_out, con
   a.Hkv = Hkv;
   a.rotate = rope ? 1 : 0;
   if (p.tokens == 0) return PKV_OK;
+  a.groups = cu_seqlens_new ? (p.tokens >> p.block_shift) + 2 * static_cast<int64_t>(batch)
+                            : batch * dense_groups(n_new, p.block_shift);
+  // slots that P pieces per thread cover, and the blocks of threads that a
+  // cache block then takes
+  const int per_p = kRopeThreads / (D / 16) / 2;
+  const int P = block_size <= per_p ? 1 : 2;  // (4: two blocks of threads per SM, a quarter slower)
+  a.cluster = static_cast<int>(ceil_div(block_size, P * per_p));
+  // one head per block of threads while that fills the device a few times over
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
-  a.groups = (p.tokens >> p.block_shift) + 2 * static_cast<int64_t>(batch);
-  a.kv_blocks = a.groups * Hkv;
-  p.per_block = rope_per_block(p.tokens, dev);
-  const int64_t blocks = a.kv_blocks + (p.x[0].heads ? ceil_div(p.tokens, p.per_block) : 0);
+  const int64_t many = 3 * static_cast<int64_t>(sm_count(dev));
+  a.heads = 1;
+  while (a.heads < Hkv && a.heads < kAppendHeads && a.groups * a.cluster * ceil_div(Hkv, 2 * a.heads) >= many)
+    a.heads *= 2;
+  a.kv_blocks = a.groups * ceil_div(Hkv, a.heads) * a.cluster;
+  p.chunks = 1;
+  if (p.x[0].heads) rope_chunks(&p);
+  int64_t blocks = a.kv_blocks + (p.x[0].heads ? ceil_div(p.tokens * p.chunks, kRopeWarps) : 0);
+  blocks = ceil_div(blocks, a.cluster) * a.cluster;  // (a warp past the last query row returns at once)
   if (blocks > INT32_MAX) return PKV_ERR_ARG;
-  append_q8_kernel<<<static_cast<unsigned>(blocks), kRopeThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(a.cluster);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(kRopeThreads);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = &attr;
+  cfg.numAttrs = a.cluster > 1 ? 1 : 0;
+  auto kern = P == 1 ? append_q8_kernel<1> : append_q8_kernel<2>;
+  return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess && cudaGetLastError() == cudaSuccess ? PKV_OK
+                                                                                           : PKV_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -10,8 +10,12 @@
 // fraction's sine and cosine are fp32 (sincospif), y is rounded to bf16 once.
 //
 // What bounds it: bytes.  A row is read and written once and the arithmetic is
-// 3 operations per element; one sine and cosine serves all heads of a token
-// through shared memory.
+// 3 operations per element.  A warp takes kRopePasses passes of rows of one
+// token (12 rows at head_dim 128), all their loads in flight before the
+// position's table look-up and the sines, which it works out once for them; no
+// barrier, so that one warp's look-ups hide behind the rows of others (blocks
+// of four tokens that shared the sines through barriers: 52 us for 16389
+// tokens of 20 heads, 168 MB).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -25,8 +29,10 @@
 namespace pkv {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeMaxTokens = 8;  // tokens per block
-constexpr int kRopeBatch = 2;      // rows a thread has in flight
+constexpr int kRopeWarps = kRopeThreads / 32;
+// Rows a lane has in flight at most: 3 leave four blocks of threads per SM
+// (16389 tokens of 20 heads: 1: 37 us, 2: 32, 3: 29, 4: 36).
+constexpr int kRopePasses = 3;
 
 struct RopeFreq {
   const float *inv_freq;  // [half]
@@ -61,7 +67,7 @@ struct RopeParams {
   const int32_t *block_table;
   int64_t bt_stride, num_blocks;
   int max_blocks_per_seq, block_shift;
-  int per_block;  // tokens per block
+  int chunks, passes;  // warps per token, passes of rows in each
   int32_t *err;
 };
 
@@ -123,7 +129,7 @@ __device__ __forceinline__ void turn_piece(const RopeFreq &f, const float2 (&cs)
   }
 }
 
-// What a block needs to know of one of its tokens.
+// What a warp needs to know of its token.
 struct RopeToken {
   int pos;
   int ok;       // the token exists
@@ -165,6 +171,7 @@ __device__ __forceinline__ RopeToken rope_token(const RopeParams &p, int64_t r) 
   }
   const int64_t pos = static_cast<int64_t>(__ldg(p.seqlens + b)) + t;
   k.pos = static_cast<int>(pos);
+  if (!p.src_paged && !p.dst_paged) return k;
   const int64_t col = pos >> p.block_shift;
   if (pos < 0 || col >= p.max_blocks_per_seq) {
     if (p.err) atomicOr(p.err, kErrTableWidth);
@@ -177,77 +184,75 @@ __device__ __forceinline__ RopeToken rope_token(const RopeParams &p, int64_t r) 
   return k;
 }
 
-// Tokens first .. first + count - 1 of the call, by one block.
-__device__ __forceinline__ void rope_tokens(const RopeParams &p, int64_t first, int count) {
-  __shared__ RopeToken tok[kRopeMaxTokens];
-  __shared__ __align__(16) float2 cs[kRopeMaxTokens][64];
-  const int tid = threadIdx.x;
-  if (tid < count) tok[tid] = rope_token(p, first + tid);
-  __syncthreads();
-  for (int i = tid; i < count * p.f.half; i += kRopeThreads) {
-    const int k = i / p.f.half, j = i - k * p.f.half;
-    cs[k][j] = rope_cs(p.f, tok[k].pos, j);
-  }
-  __syncthreads();
-  const int U = p.D >> 4, u = tid % U;  // pieces per row; a thread keeps its piece index
+// Warp `item` of the call: p.passes passes of 32 / U rows of one token.
+// cs: the warp's 64 cosines and sines.
+__device__ __forceinline__ void rope_warp(const RopeParams &p, int64_t item, float2 *cs) {
+  const int lane = threadIdx.x & 31;
+  const int64_t r = item / p.chunks;
+  if (r >= p.tokens) return;
+  const int U = p.D >> 4, u = lane & (U - 1);  // pieces per row; a lane keeps its piece index
+  const int per_pass = 32 / U, h0 = static_cast<int>(item - r * p.chunks) * p.passes * per_pass + lane / U;
   const int2 ch = piece_chunks(p.f, u);
   const bool turns = 16 * u < 2 * p.f.half;
   const int rows = p.x[0].heads + p.x[1].heads + p.x[2].heads;
-  for (int k = 0; k < count; ++k) {
-    const RopeToken T = tok[k];
-    if (!T.ok) continue;
-    float2 c[8];
-    if (turns) {
+  const RopeToken T = rope_token(p, r);
+  if (!T.ok) return;  // warp-uniform
+  uint4 a[kRopePasses], b[kRopePasses];
+  uint16_t *dst[kRopePasses];
+  bool turn[kRopePasses];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) c[e] = cs[k][8 * u + e];
-    }
-    // kRopeBatch rows' loads go out together (an output may be its input, so
-    // the compiler may not move a load over a store by itself)
-    for (int h0 = tid / U; h0 < rows; h0 += kRopeBatch * (kRopeThreads / U)) {
-      uint4 a[kRopeBatch], b[kRopeBatch];
-      uint16_t *dst[kRopeBatch];
-      bool turn[kRopeBatch];
-#pragma unroll
-      for (int q = 0; q < kRopeBatch; ++q) {
-        const int h = h0 + q * (kRopeThreads / U);
-        dst[q] = nullptr;
-        turn[q] = false;
-        a[q] = b[q] = make_uint4(0u, 0u, 0u, 0u);
-        if (h >= rows) continue;
-        const int w = h < p.x[0].heads ? 0 : h < p.x[0].heads + p.x[1].heads ? 1 : 2;
-        const RopeRows &X = p.x[w];
-        const int head = h - (w > 0 ? p.x[0].heads : 0) - (w > 1 ? p.x[1].heads : 0);
-        const bool sp = w > 0 && p.src_paged, dp = w > 0 && p.dst_paged;
-        if (dp && !T.in_cache) continue;
+  for (int q = 0; q < kRopePasses; ++q) {
+    const int h = h0 + q * per_pass;
+    dst[q] = nullptr;
+    turn[q] = false;
+    a[q] = b[q] = make_uint4(0u, 0u, 0u, 0u);
+    if (q < p.passes && h < rows) {
+      const int w = h < p.x[0].heads ? 0 : h < p.x[0].heads + p.x[1].heads ? 1 : 2;
+      const RopeRows &X = p.x[w];
+      const int head = h - (w > 0 ? p.x[0].heads : 0) - (w > 1 ? p.x[1].heads : 0);
+      const bool sp = w > 0 && p.src_paged, dp = w > 0 && p.dst_paged;
+      if (!dp || T.in_cache) {
         dst[q] = X.dst + (dp ? T.blk : T.b) * X.d0 + (dp ? T.slot : T.t) * X.d1 + head * X.d2;
         turn[q] = X.rotate && turns;
-        if (sp && !T.in_cache) continue;  // (zeros)
-        const uint4 *s = reinterpret_cast<const uint4 *>(
-            X.src + (sp ? T.blk : T.b) * X.s0 + (sp ? T.slot : T.t) * X.s1 + head * X.s2);
-        a[q] = s[ch.x];
-        b[q] = s[ch.y];
-      }
-#pragma unroll
-      for (int q = 0; q < kRopeBatch; ++q) {
-        if (!dst[q]) continue;
-        if (turn[q]) {
-          float v[16];
-          turn_piece(p.f, c, a[q], b[q], v);
-          a[q] = make_uint4(bf2_of(v[0], v[1]), bf2_of(v[2], v[3]), bf2_of(v[4], v[5]), bf2_of(v[6], v[7]));
-          b[q] = make_uint4(bf2_of(v[8], v[9]), bf2_of(v[10], v[11]), bf2_of(v[12], v[13]),
-                            bf2_of(v[14], v[15]));
+        if (!sp || T.in_cache) {  // (otherwise zeros)
+          const uint4 *s = reinterpret_cast<const uint4 *>(
+              X.src + (sp ? T.blk : T.b) * X.s0 + (sp ? T.slot : T.t) * X.s1 + head * X.s2);
+          a[q] = s[ch.x];
+          b[q] = s[ch.y];
         }
-        reinterpret_cast<uint4 *>(dst[q])[ch.x] = a[q];
-        reinterpret_cast<uint4 *>(dst[q])[ch.y] = b[q];
       }
     }
   }
+  for (int i = lane; i < p.f.half; i += 32) cs[i] = rope_cs(p.f, T.pos, i);
+  __syncwarp();
+  float2 c[8];
+  if (turns) {
+    const float4 *c4 = reinterpret_cast<const float4 *>(cs + 8 * u);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float4 v = c4[e];
+      c[2 * e] = make_float2(v.x, v.y);
+      c[2 * e + 1] = make_float2(v.z, v.w);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < kRopePasses; ++q) {
+    if (!dst[q]) continue;
+    if (turn[q]) {
+      float v[16];
+      turn_piece(p.f, c, a[q], b[q], v);
+      a[q] = make_uint4(bf2_of(v[0], v[1]), bf2_of(v[2], v[3]), bf2_of(v[4], v[5]), bf2_of(v[6], v[7]));
+      b[q] = make_uint4(bf2_of(v[8], v[9]), bf2_of(v[10], v[11]), bf2_of(v[12], v[13]), bf2_of(v[14], v[15]));
+    }
+    reinterpret_cast<uint4 *>(dst[q])[ch.x] = a[q];
+    reinterpret_cast<uint4 *>(dst[q])[ch.y] = b[q];
+  }
 }
 
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * p.per_block;
-  const int64_t left = p.tokens - first;
-  rope_tokens(p, first, static_cast<int>(left < p.per_block ? left : p.per_block));
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_constant__ RopeParams p) {
+  __shared__ __align__(16) float2 cs[kRopeWarps][64];
+  const int warp = threadIdx.x >> 5;
+  rope_warp(p, static_cast<int64_t>(blockIdx.x) * kRopeWarps + warp, cs[warp]);
 }
 
 }  // namespace pkv

@@ -6,8 +6,8 @@ table of inverse frequencies on the host.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import math
 from typing import Optional, Tuple, Union
 
@@ -71,19 +71,46 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: Optiona
     return f.to(torch.float32).to(device), m
 
 
-@contextlib.contextmanager
-def _on(device: torch.device, stream):
+class _on:
     """The tensors' device and the call's stream made current: outputs and
-    workspaces are allocated for the stream that uses them.  Yields the handle."""
-    with torch.cuda.device(device):
+    workspaces are allocated for the stream that uses them.  Entering gives the
+    stream's handle.  (A class, and nothing switched when both are current
+    already: the host's share of a small call is most of its time.)"""
+
+    __slots__ = ("device", "stream", "inside")
+
+    def __init__(self, device: torch.device, stream):
+        self.device, self.stream, self.inside = device, stream, None
+
+    def __enter__(self) -> int:
+        index = self.device.index
+        if self.stream is None and index == torch.cuda.current_device():
+            return _stream_handle(None) if _raw_stream is None else _raw_stream(index)
+        guard = torch.cuda.device(self.device)
+        guard.__enter__()
+        self.inside = [guard]
+        stream = self.stream
         if stream is None:
-            yield _stream_handle(None)
-            return
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else \
-                torch.cuda.default_stream(device)
-        with torch.cuda.stream(stream):
-            yield _stream_handle(stream)
+            return _stream_handle(None)
+        try:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=self.device) if int(stream) else \
+                    torch.cuda.default_stream(self.device)
+            switch = torch.cuda.stream(stream)
+            switch.__enter__()
+        except BaseException:
+            guard.__exit__(None, None, None)
+            raise
+        self.inside.append(switch)
+        return _stream_handle(stream)
+
+    def __exit__(self, *exc) -> None:
+        for ctx in reversed(self.inside or ()):
+            ctx.__exit__(*exc)
+
+
+# the current stream's handle without a Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _need_freq(inv_freq: torch.Tensor, D: int) -> None:
@@ -117,13 +144,17 @@ def _need_tokens(name: str, t: torch.Tensor, packed: bool, lead=None, tail=None)
         raise ValueError(f"{name} has shape {tuple(t.shape)}: it disagrees with the other tensors")
 
 
+@functools.lru_cache(maxsize=4096)
+def _stride_array(strides: tuple, shape: tuple) -> ctypes.Array:
+    st = [s if n > 1 else max(s, 1) * 16 for s, n in zip(strides, shape)][:-1]
+    return (ctypes.c_int64 * 3)(*([st[0]] + st if len(st) == 2 else st))
+
+
 def _strides(t: Optional[torch.Tensor]):
     """(batch, token, head) strides; a packed tensor repeats its token stride.
-    Axes of size 1 are never stepped over and get a stride that passes."""
-    if t is None:
-        return None
-    st = [int(s) if n > 1 else max(int(s), 1) * 16 for s, n in zip(t.stride(), t.shape)][:-1]
-    return (ctypes.c_int64 * 3)(*([st[0]] + st if t.dim() == 3 else st))
+    Axes of size 1 are never stepped over and get a stride that passes.  (The
+    arrays are shared between calls: nothing writes to them.)"""
+    return None if t is None else _stride_array(t.stride(), t.shape)
 
 
 def rope(q: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, *,
@@ -148,8 +179,7 @@ def rope(q: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, *,
         raise ValueError(f"positions must be a contiguous {tuple(lead)} tensor")
     _need_freq(inv_freq, D)
     par = _params(inv_freq, interleaved, mscale)
-    L = lib()
-    fn = L.pkv_rope
+    fn = lib().pkv_rope
     if not fn.argtypes:
         fn.argtypes = [_P, _P, _P, _P, _I, _P, _P, _P, _P, _I, _P, _I, _I, _I, _P, _I, _P]
         fn.restype = _I
@@ -221,8 +251,7 @@ def kv_append_rope(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tens
     par = _params(inv_freq, interleaved, mscale)
     _need_one_device(k_new, v_new, k_cache, v_cache, block_table, seqlens, inv_freq, q,
                      cu_seqlens_new, q_out, err)
-    L = lib()
-    fn = L.pkv_kv_append_rope
+    fn = lib().pkv_kv_append_rope
     if not fn.argtypes:
         fn.argtypes = [_P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _I, _P, _P, _P, _P, _I64, _P, _I64,
                        _I, _P, _I, _I, _I, _I, _I, _P, _P, _P]
@@ -291,8 +320,7 @@ def kv_append_rope_bwd(dq_rot: Optional[torch.Tensor], dk_cache: torch.Tensor,
     par = _params(inv_freq, interleaved, mscale)
     _need_one_device(dk_cache, dv_cache, block_table, seqlens, inv_freq, dq_rot, cu_seqlens_new,
                      dq, dk_new, dv_new, err)
-    L = lib()
-    fn = L.pkv_kv_append_rope_bwd
+    fn = lib().pkv_kv_append_rope_bwd
     if not fn.argtypes:
         fn.argtypes = [_P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I64, _P, _I64,
                        _I, _P, _I, _I, _I, _I, _I, _P, _P, _P]
