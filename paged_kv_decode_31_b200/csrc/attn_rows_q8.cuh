@@ -22,9 +22,13 @@
 // leaves TMEM for a third S buffer.  V is widened because P in fp16 needs an
 // fp16 partner; K is read in place.
 //
-// What bounds it: the softmax's instructions (per element a maximum, a fused
-// multiply-add, an exponential, an addition and half a conversion), as in the
-// bf16 kernel.
+// What bounds it: the softmax warps and the instruction cache (8 x 512 queries
+// at context 2048, Hq 16 / Hkv 4, D 128: 159 us, 378 TFLOP/s; tensor pipe 15 %
+// of the cycles, exponentials 16 %, instruction-cache hits 71 % before the loops
+// below were kept rolled, which was worth 10 %).  Measured and dropped: the two
+// softmax warpgroups on alternate tiles (174 us), one 16-key group in flight
+// ahead of the one in use (197), a whole row of S in registers (304: unrolled
+// 128 wide, it leaves the instruction cache at every pass).
 //
 // Roles (640 threads): warps 0-3 / 4-7 softmax (thread t = row t, keys [0, 64)
 // and [64, 128) of every tile), 8-11 epilogue, 12-15 converters (V to fp16, and
@@ -153,7 +157,7 @@ __device__ __forceinline__ void convert_q_row(const Q8Params &p, const Unit &x, 
 template <int D>
 __device__ __forceinline__ void convert_v(const uint8_t *src, uint8_t *dst, int held, int t) {
   constexpr int kCh = D / 16;  // 16-byte chunks of a row
-#pragma unroll 4
+#pragma unroll 2
   for (int i = t; i < kTileTokens * kCh; i += 128) {
     const int tok = i / kCh, c = i % kCh;
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -443,7 +447,7 @@ __global__ void __launch_bounds__(kR8Threads, 1)
         __syncwarp();
         const bool full = __all_sync(0xffffffffu, nvis == kTileTokens);  // warp-uniform
         float hm = NEG_INF;
-#pragma unroll
+#pragma unroll 1
         for (int q = 0; q < 4; q += 2) {
           float v0[16], v1[16];
           tmem_ld16(srow + 64 * wg + 16 * q, v0);
@@ -463,8 +467,9 @@ __global__ void __launch_bounds__(kR8Threads, 1)
             r0 = fmaxf(r0, v0[e]);
             r1 = fmaxf(r1, v1[e]);
           }
-          if (r0 != NEG_INF) hm = fmaxf(hm, __fmaf_rn(r0, f[q], ev[q]));
-          if (r1 != NEG_INF) hm = fmaxf(hm, __fmaf_rn(r1, f[q + 1], ev[q + 1]));
+          const float fa = q ? f[2] : f[0], fb = q ? f[3] : f[1], ea = q ? ev[2] : ev[0], eb = q ? ev[3] : ev[1];
+          if (r0 != NEG_INF) hm = fmaxf(hm, __fmaf_rn(r0, fa, ea));
+          if (r1 != NEG_INF) hm = fmaxf(hm, __fmaf_rn(r1, fb, eb));
         }
         sm->xmax[gi & 1][wg][t] = hm;
         if (named_bar_or(kXchgBar, 256, !ok)) {
@@ -498,7 +503,7 @@ __global__ void __launch_bounds__(kR8Threads, 1)
         }
         // pass 2: P over S, and this half's sum of P 2^-ev
         float half = 0.f;
-#pragma unroll
+#pragma unroll 1
         for (int g2 = 0; g2 < 2; ++g2) {  // 32 keys
           float v[2][16];
           tmem_ld16(srow + 64 * wg + 32 * g2, v[0]);
@@ -509,9 +514,10 @@ __global__ void __launch_bounds__(kR8Threads, 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int q = 2 * g2 + h;
-            const float c = __fsub_rn(ev[q], m_new);
+            const float fq = g2 ? f[2 + h] : f[h], iq = g2 ? iv[2 + h] : iv[h];
+            const float c = __fsub_rn(g2 ? ev[2 + h] : ev[h], m_new);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[h][e] = ex2(__fmaf_rn(v[h][e], f[q], c));
+            for (int e = 0; e < 16; ++e) v[h][e] = ex2(__fmaf_rn(v[h][e], fq, c));
             if (!full) {
 #pragma unroll
               for (int e = 0; e < 16; ++e)
@@ -526,7 +532,7 @@ __global__ void __launch_bounds__(kR8Threads, 1)
             for (int off = 8; off >= 1; off >>= 1)
 #pragma unroll
               for (int e = 0; e < off; ++e) v[h][e] = __fadd_rn(v[h][e], v[h][e + off]);
-            half = __fmaf_rn(v[h][0], iv[q], half);
+            half = __fmaf_rn(v[h][0], iq, half);
           }
           tmem_st16(srow + 64 * wg + 32 * g2, w);
         }
