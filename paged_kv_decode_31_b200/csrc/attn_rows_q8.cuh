@@ -241,9 +241,8 @@ __global__ void __launch_bounds__(kR8Threads, 1)
                                    start->sched_list, start->sched_meta, &start->sched_count);
       if (start->sched_count >= 0) deal = Sched{start->sched_list, start->sched_meta, start->sched_count};
     }
-    sc = Sched8{deal.count <= kSchedMaxMine ? sm->units : nullptr, deal.count};
-    if (sc.units)
-      for (int k = threadIdx.x; k < sc.count; k += kR8Threads) sm->units[k] = deal.get<kRowsPerTile>(p, k);
+    sc = Sched8{sm->units, min(deal.count, kSchedMaxMine)};
+    for (int k = threadIdx.x; k < sc.count; k += kR8Threads) sm->units[k] = deal.get<kRowsPerTile>(p, k);
     __syncthreads();  // (also: the start-up data's place is free)
   }
 
@@ -256,8 +255,8 @@ __global__ void __launch_bounds__(kR8Threads, 1)
     } else if (warp == C::kPrep) {
       int kb[kTabBatch], vb[kTabBatch];
       Unit x;
-      for (int k = next_unit8<kRowsPerTile>(p, sc, 0, x), ui = 0; k >= 0;
-           k = next_unit8<kRowsPerTile>(p, sc, k + 1, x), ++ui) {
+      for (int k = next_unit8(sc, 0, x), ui = 0; k >= 0;
+           k = next_unit8(sc, k + 1, x), ++ui) {
         const int us = ui % C::kUS;
         bool ok = true;
         if (lane == 0) ok = mbar_wait(&sm->tab_free[us], ((ui / C::kUS) & 1) ^ 1, abort_any, p.wait_ns);
@@ -304,7 +303,7 @@ __global__ void __launch_bounds__(kR8Threads, 1)
         return true;
       };
       for (int k = 0; k < sc.count && !failed; ++k) {
-        const Unit x = unit8<kRowsPerTile>(p, sc, k);
+        const Unit x = sc.units[k];
         if (x.n_tiles == 0) continue;
         const int qb = ui & 1;
         if (!mbar_wait(&sm->q_full[qb], (ui >> 1) & 1, abort_any, p.wait_ns)) {
@@ -356,7 +355,7 @@ __global__ void __launch_bounds__(kR8Threads, 1)
     regs_dec<kR8ConvRegs>();
     const int t = threadIdx.x & 127;
     Unit cur, nxt;
-    int k = next_unit8<kRowsPerTile>(p, sc, 0, cur), gi = 0;
+    int k = next_unit8(sc, 0, cur), gi = 0;
     bool failed = false;
     auto put_q = [&](const Unit &x, int ord) {
       const int qb = ord & 1;
@@ -369,7 +368,7 @@ __global__ void __launch_bounds__(kR8Threads, 1)
     };
     if (k >= 0) failed = !put_q(cur, 0);
     for (int ui = 0; k >= 0 && !failed; ++ui) {
-      const int nk = next_unit8<kRowsPerTile>(p, sc, k + 1, nxt);
+      const int nk = next_unit8(sc, k + 1, nxt);
       for (int j = 0; j < cur.n_tiles; ++j, ++gi) {
         const int st = gi % NSV, sh = gi % NSH;
         if (!mbar_wait(&sm->full_v[st], (gi / NSV) & 1, abort_any, p.wait_ns) ||
@@ -407,7 +406,7 @@ __global__ void __launch_bounds__(kR8Threads, 1)
     int gbase = 0, uo = 0;
     bool stop = false;
     for (int k = 0; k < sc.count && !stop; ++k) {
-      const Unit x = unit8<kRowsPerTile>(p, sc, k);
+      const Unit x = sc.units[k];
       if (x.n_tiles == 0) continue;
       int nlim = 0;  // keys [0, nlim) are visible to row t
       if (t < x.rows) {
@@ -579,7 +578,7 @@ __global__ void __launch_bounds__(kR8Threads, 1)
     float acc[D];
     int uo = 0;
     for (int k = 0; k < sc.count; ++k) {
-      const Unit x = unit8<kRowsPerTile>(p, sc, k);
+      const Unit x = sc.units[k];
       if (t == 0) check_sequence(p, x);
       if (x.n_tiles == 0) {
         // rows that see no key: out = 0, lse = -inf (by the unit of split 0)

@@ -273,29 +273,18 @@ __device__ __forceinline__ void put_q_pass(const Q8Params &p, uint4 v, int c, ui
   if (ch == 0) rowf[c] = __fmul_rn(p.cscale, qs.back);
 }
 
-// The units of this CTA: from shared memory, where they were worked out once
-// (the divisions of unit_make in every role would be most of the kernel's
-// code), or, when they are more than fit there, by a function call.
+// The units of this CTA, in shared memory, where they were worked out once (the
+// divisions of unit_make in every role would be most of the kernel's code).
+// The host's grid leaves a CTA at most kSchedMaxMine of them.
 struct Sched8 {
   const Unit *units;
   int count;
 };
 
-template <int N>
-__device__ __noinline__ Unit strided_unit(const Q8Params &p, int k) {
-  return unit_at<N>(p, static_cast<int>(blockIdx.x) + k * static_cast<int>(gridDim.x));
-}
-
-template <int N>
-__device__ __forceinline__ Unit unit8(const Q8Params &p, const Sched8 &sc, int k) {
-  return sc.units ? sc.units[k] : strided_unit<N>(p, k);
-}
-
 // First unit with tiles at or after `from`, or -1.
-template <int N>
-__device__ __forceinline__ int next_unit8(const Q8Params &p, const Sched8 &sc, int from, Unit &out) {
+__device__ __forceinline__ int next_unit8(const Sched8 &sc, int from, Unit &out) {
   for (int k = from; k < sc.count; ++k) {
-    out = unit8<N>(p, sc, k);
+    out = sc.units[k];
     if (out.n_tiles > 0) return k;
   }
   return -1;
@@ -314,12 +303,12 @@ __device__ __forceinline__ void prepare_q8(const Q8Params &p, uint8_t *smem, typ
     return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
   };
   Unit cur, nxt;
-  int k = next_unit8<N>(p, sc, 0, cur);
+  int k = next_unit8(sc, 0, cur);
   if (k >= 0) fetch_tab(p, cur, sm->tab[0], lane);
   cp_async_commit();
   int kb[kTabBatch], vb[kTabBatch];
   for (int ui = 0; k >= 0; ++ui) {
-    const int nk = next_unit8<N>(p, sc, k + 1, nxt);
+    const int nk = next_unit8(sc, k + 1, nxt);
     // this unit's query rows, and the next unit's table
 #pragma unroll 1
     for (int c = lane / kLanes; c < cur.rows; c += kRows)
@@ -377,8 +366,8 @@ __device__ __forceinline__ void load_q8(const Q8Params &p, const CUtensorMap *ma
   int gi = 0;
   bool failed = false;
   Unit x;
-  for (int k = next_unit8<N>(p, sc, 0, x), ui = 0; k >= 0 && !failed;
-       k = next_unit8<N>(p, sc, k + 1, x), ++ui) {
+  for (int k = next_unit8(sc, 0, x), ui = 0; k >= 0 && !failed;
+       k = next_unit8(sc, k + 1, x), ++ui) {
     bool okt = true;
     if (lane == 0) okt = mbar_wait_call(&sm->tab_full[ui % US], (ui / US) & 1, abort_any, p.wait_ns);
     if (!__shfl_sync(0xffffffffu, okt ? 1 : 0, 0)) break;
@@ -499,11 +488,9 @@ __global__ void __launch_bounds__(32 * Q8Cfg<D, N, NSK, NSV>::kWarps, 1)
                         sm->sched_list, sm->sched_meta, &sm->sched_count);
       if (sm->sched_count >= 0) deal = Sched{sm->sched_list, sm->sched_meta, sm->sched_count};
     }
-    sc = Sched8{deal.count <= kSchedMaxMine ? sm->units : nullptr, deal.count};
-    if (sc.units) {
-      for (int k = threadIdx.x; k < sc.count; k += blockDim.x) sm->units[k] = deal.get<N>(p, k);
-      __syncthreads();
-    }
+    sc = Sched8{sm->units, min(deal.count, kSchedMaxMine)};
+    for (int k = threadIdx.x; k < sc.count; k += blockDim.x) sm->units[k] = deal.get<N>(p, k);
+    __syncthreads();
   }
 
   if (warp == C::kPrepW) {
@@ -531,7 +518,7 @@ __global__ void __launch_bounds__(32 * Q8Cfg<D, N, NSK, NSV>::kWarps, 1)
       int gi = 0, pi = 0, ui = 0;
       bool failed = false;
       for (int k = 0; k < sc.count && !failed; ++k) {
-        const Unit x = unit8<N>(p, sc, k);
+        const Unit x = sc.units[k];
         if (x.n_tiles == 0) continue;
         if (is_qk) {
           const int qb = ui % QB;
@@ -614,7 +601,7 @@ __global__ void __launch_bounds__(32 * Q8Cfg<D, N, NSK, NSV>::kWarps, 1)
     int gbase = 0, pbase = 0, uo = 0;  // uo: ordinal of the unit among this CTA's units with work
     bool stop = false;
     for (int k = 0; k < sc.count && !stop; ++k) {
-      const Unit x = unit8<N>(p, sc, k);
+      const Unit x = sc.units[k];
       if (x.n_tiles == 0) continue;
       const uint32_t ocol = tmem + lane_off + C::kColO + (uo & 1) * C::kPCols;  // this unit's O^T
       if (t < N) {
@@ -839,7 +826,7 @@ __global__ void __launch_bounds__(32 * Q8Cfg<D, N, NSK, NSV>::kWarps, 1)
     bool bulk_out = false;   // thread 0 has bulk stores to complete before exit
     bool stop = false;
     for (int k = 0; k < sc.count && !stop; ++k) {
-      const Unit x = unit8<N>(p, sc, k);
+      const Unit x = sc.units[k];
       if (t == 0) check_sequence(p, x);
       if (x.n_tiles == 0) {
         // direct write: rows of this unit see no key (out = 0, lse = -inf)

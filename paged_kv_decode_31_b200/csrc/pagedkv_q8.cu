@@ -67,6 +67,13 @@ constexpr int v_stages() {
   return D == 128 ? 6 : 10;
 }
 
+// One CTA per SM, each with at most kSchedMaxMine units: more units than that
+// take more CTAs (the later ones queue; none waits for another).
+int q8_grid(const Q8Params &p, int dev) {
+  const int sms = sm_count(dev), least = static_cast<int>(ceil_div(p.n_units, kSchedMaxMine));
+  return least > sms ? least : p.n_units < sms ? p.n_units : sms;
+}
+
 template <int D, int N>
 int launch_split_q8(const Q8Params &p, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t s,
                     int dev) {
@@ -81,7 +88,7 @@ int launch_split_q8(const Q8Params &p, const CUtensorMap &mk, const CUtensorMap 
       return PKV_ERR_CUDA;
     if (dev >= 0 && dev < kMaxDevices) attr_set[dev].store(true, std::memory_order_release);
   }
-  const int grid = p.n_units < sm_count(dev) ? p.n_units : sm_count(dev);
+  const int grid = q8_grid(p, dev);
   Q8Params pp = p;
   pp.sched = p.n_units <= C::kSchedScratch ? 1 : 0;
   kern<<<grid, 32 * C::kWarps, C::kSmemBytes, s>>>(pp, mk, mv);
@@ -117,7 +124,7 @@ int launch_rows_q8(const Q8Params &p, const CUtensorMap &mk, const CUtensorMap &
       return PKV_ERR_CUDA;
     if (dev >= 0 && dev < kMaxDevices) attr_set[dev].store(true, std::memory_order_release);
   }
-  const int grid = p.n_units < sm_count(dev) ? p.n_units : sm_count(dev);
+  const int grid = q8_grid(p, dev);
   Q8Params pp = p;
   pp.sched = p.n_units <= C::kSchedScratch ? 1 : 0;
   kern<<<grid, kR8Threads, C::kSmemBytes, s>>>(pp, mk, mv);
