@@ -89,7 +89,7 @@ struct RowCfg {
     int tab[2][2][kSplitTokens / 16];
     int sched_list[kSchedMaxMine];     // this CTA's units (balanced schedule)
     int sched_meta[kSchedMaxMine][3];  // their sequence length and query range
-    int sched_hist[kSchedHist], sched_start[kSchedBuckets];
+    int sched_hist[kSchedHist];
     int sched_count;
   };
   static constexpr int kSmemBytes = kOffSmall + static_cast<int>(sizeof(Small)) + 1024;
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
   Sched sc = strided_sched(p);
   if (p.sched) {
     build_schedule<kRowsPerTile>(p, smem + C::kOffQ, C::kSchedScratch, sm->sched_hist,
-                                 sm->sched_start, sm->sched_list, sm->sched_meta, &sm->sched_count);
+                                 sm->sched_list, sm->sched_meta, &sm->sched_count);
     if (sm->sched_count >= 0) sc = Sched{sm->sched_list, sm->sched_meta, sm->sched_count};
   }
 

@@ -22,13 +22,16 @@
 // leaves TMEM for a third S buffer.  V is widened because P in fp16 needs an
 // fp16 partner; K is read in place.
 //
-// What bounds it: the softmax warps and the instruction cache (8 x 512 queries
-// at context 2048, Hq 16 / Hkv 4, D 128: 159 us, 378 TFLOP/s; tensor pipe 15 %
-// of the cycles, exponentials 16 %, instruction-cache hits 71 % before the loops
-// below were kept rolled, which was worth 10 %).  Measured and dropped: the two
-// softmax warpgroups on alternate tiles (174 us), one 16-key group in flight
-// ahead of the one in use (197), a whole row of S in registers (304: unrolled
-// 128 wide, it leaves the instruction cache at every pass).
+// What bounds it: issue slots and the instruction cache.  8 x 512 queries at
+// context 2048, Hq 16 / Hkv 4, D 128: 136 us, 442 TFLOP/s; 3300 cycles a tile,
+// of which the softmax's two passes take 2200, with the tensor pipe near 20 %.
+// Code that stays small is what made it fast (start: 175 us): rolled softmax
+// loops (-16), query rows converted a few at a time between V tiles and an
+// epilogue of rolled 16-column steps without registers of its own for O, which
+// also leaves the softmax 128 registers (-24).  Measured and dropped: the two
+// softmax warpgroups on alternate tiles (equal), 16 keys in flight ahead of
+// those in use (+22), S kept in registers between the passes (+32), either
+// pass unrolled (+2, +5), scales read inside the loops (+6).
 //
 // Roles (640 threads): warps 0-3 / 4-7 softmax (thread t = row t, keys [0, 64)
 // and [64, 128) of every tile), 8-11 epilogue, 12-15 converters (V to fp16, and
@@ -43,7 +46,7 @@ namespace pkv {
 
 constexpr int kR8Threads = 640;
 // Registers per thread: at launch, and each warpgroup's share of their sum.
-constexpr int kR8LaunchRegs = 96, kR8SoftmaxRegs = 88, kR8EpiRegs = 176, kR8ConvRegs = 64, kR8AuxRegs = 64;
+constexpr int kR8LaunchRegs = 96, kR8SoftmaxRegs = 128, kR8EpiRegs = 88, kR8ConvRegs = 72, kR8AuxRegs = 64;
 static_assert(2 * kR8SoftmaxRegs + kR8EpiRegs + kR8ConvRegs + kR8AuxRegs == 5 * kR8LaunchRegs,
               "warpgroup register shares must add up to the launch allocation");
 
@@ -68,7 +71,7 @@ struct R8Cfg {
   // also only at kernel start, in the fp16 tiles' place
   struct Start {
     int sched_list[kSchedMaxMine], sched_meta[kSchedMaxMine][3];
-    int sched_hist[kSchedHist], sched_start[kSchedBuckets], sched_count;
+    int sched_hist[kSchedHist], sched_count;
   };
   static_assert(sizeof(Start) <= NSH * kHBytes, "start-up data");
   struct Small {
@@ -92,64 +95,114 @@ struct R8Cfg {
   static constexpr uint32_t kColO = kSB * 128;
 };
 
-// Row t of a 128-row tile: out / lse through the merge's fold of one split, or
-// the split partial.  acc: the row's O, read from TMEM by the caller.
-template <int D>
-__device__ __forceinline__ void finish_row_q8(const Q8Params &p, const Unit &x, int t, float m, float l,
-                                              const float (&acc)[D]) {
-  const int i = (x.row0 + t) / p.G;
+// The end of row t of a 128-row tile: out and lse where the row has one split
+// (the fold of one partial is the partial), else the partial.  16 columns of O
+// at a time, in a loop that stays rolled: unrolled over the head it drove the
+// softmax out of the instruction cache, and four to six tiles of every unit
+// took half as long again.  out = O * (1 / l), not the merge's correctly
+// rounded quotient: within 2^-23 of it before the rounding to bf16, and a
+// tenth of the instructions while the softmax warps need every issue slot.
+struct RowEnd {
+  __nv_bfloat16 *out, *fin;  // final row (fin: the sequence's last row, or null)
+  float *part;               // split partial (out is null)
+  float inv;                 // 1 / l, 0 for a row that saw no key
+};
+
+__device__ __forceinline__ RowEnd row_end(const Q8Params &p, const Unit &x, int t, float m, float l, int D) {
+  RowEnd r{};
+  const int i = (x.row0 + t) / p.G, g = x.row0 + t - i * p.G, h = x.kvh * p.G + g;
   int lim = x.seqlen;
   if (p.causal) lim = min(lim, x.seqlen - x.nq + i + 1);
-  if (lim <= kSplitTokens) {
-    if (x.s == 0) write_final_row<D>(p, x, t, m, l, acc);
-    return;
+  if (lim > kSplitTokens) {
+    const int64_t slot = ((x.q0 + i) * p.Hq + h) * static_cast<int64_t>(p.n_splits) + x.s;
+    r.part = p.ws_acc + slot * D;
+    *reinterpret_cast<float2 *>(p.ws_ml + slot * 2) = make_float2(m, l);
+    return r;
   }
-  const int g = x.row0 + t - i * p.G;
-  const int64_t slot = ((x.q0 + i) * p.Hq + x.kvh * p.G + g) * static_cast<int64_t>(p.n_splits) + x.s;
-  float4 *dst = reinterpret_cast<float4 *>(p.ws_acc + slot * D);
-#pragma unroll
-  for (int c4 = 0; c4 < D / 4; ++c4)
-    dst[c4] = make_float4(acc[4 * c4], acc[4 * c4 + 1], acc[4 * c4 + 2], acc[4 * c4 + 3]);
-  *reinterpret_cast<float2 *>(p.ws_ml + slot * 2) = make_float2(m, l);
+  if (x.s != 0) return r;
+  r.inv = final_rcp(l);
+  r.out = p.out + o_tok_off(p, x, i) + h * p.o_sh;
+  const float ls = final_lse(m, l);
+  p.lse[lse_index(p, x, i, h)] = ls;
+  if (p.fin_out != nullptr && i == x.nq - 1) {
+    r.fin = p.fin_out + x.b * p.fo_sb + h * p.fo_sh;
+    p.fin_lse[static_cast<int64_t>(x.b) * p.Hq + h] = ls;
+  }
+  return r;
 }
 
-// Query row t of unit x as q_hi and q_lo, by one thread: the largest magnitude
-// first, then the conversion of the same bytes again.
+// 16 columns of O from column c on.
+__device__ __forceinline__ void end_cols(const Q8Params &p, const RowEnd &r, int c, const float (&v)[16]) {
+  if (r.part) {
+#pragma unroll
+    for (int e = 0; e < 16; e += 4)
+      *reinterpret_cast<float4 *>(r.part + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+    return;
+  }
+  if (!r.out) return;
+  __nv_bfloat162 h2[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    h2[e] = __floats2bfloat162_rn(__fmul_rn(v[2 * e], r.inv), __fmul_rn(v[2 * e + 1], r.inv));
+  if (p.out_vec) {
+    *reinterpret_cast<uint4 *>(r.out + c) = *reinterpret_cast<uint4 *>(h2);
+    *reinterpret_cast<uint4 *>(r.out + c + 8) = *reinterpret_cast<uint4 *>(h2 + 4);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) r.out[c + e] = e & 1 ? h2[e >> 1].y : h2[e >> 1].x;
+  }
+  if (r.fin) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) r.fin[c + e] = e & 1 ? h2[e >> 1].y : h2[e >> 1].x;
+  }
+}
+
+// Query rows of unit x as q_hi and q_lo, by the converter warpgroup, in place:
+// the two halves of a row's bytes are copied to where its hi and its lo go
+// (ask_q, asynchronous), then the D / 8 lanes that share a row read it and
+// write both (put_q_pass: 1024 / D rows).  Rows past x.rows keep what the
+// buffer holds: their S is not used.
 template <int D>
-__device__ __forceinline__ void convert_q_row(const Q8Params &p, const Unit &x, int t, uint8_t *dst,
-                                              float *rowf) {
-  if (t >= x.rows) return;  // (rows past it: their S is not used)
-  const uint4 *src = q_row<D>(p, x, t);
-  uint32_t top = 0;
-#pragma unroll 4
-  for (int c = 0; c < D / 8; ++c) {
-    const uint4 v = __ldg(src + c);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
-  }
-  const QScale qs = q_scale(top);
+constexpr int kQPasses = kRowsPerTile * (D / 8) / 128;
+
+template <int D>
+__device__ __forceinline__ int raw_q_off(int r, int ch) {
+  return (ch < D / 16 ? 0 : kRowsPerTile * D) + swz16<D>(r, ch % (D / 16));
+}
+
+template <int D>
+__device__ __forceinline__ void ask_q(const Q8Params &p, const Unit &x, int t, uint8_t *dst) {
+  constexpr int kLanes = D / 8;
 #pragma unroll 1
-  for (int c = 0; c < D / 16; ++c) {
-    uint32_t hi[4], lo[4];
+  for (int c = t / kLanes; c < x.rows; c += 128 / kLanes)
+    cp_async16(dst + raw_q_off<D>(c, t % kLanes), q_row<D>(p, x, c) + t % kLanes, 16);
+  cp_async_commit();
+}
+
+template <int D>
+__device__ __forceinline__ void put_q_rows(const Q8Params &p, int pass, int t, uint8_t *dst, float *rowf) {
+  constexpr int kLanes = D / 8;
+  const int ch = t % kLanes, c = pass * (128 / kLanes) + t / kLanes;
+  const uint4 v = *reinterpret_cast<const uint4 *>(dst + raw_q_off<D>(c, ch));
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t top = 0;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint4 v = __ldg(src + 2 * c + h);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const Split2 a = split_q_one_scale(__fmul_rn(bf_lo(w[2 * e]), qs.f), __fmul_rn(bf_hi(w[2 * e]), qs.f));
-        const Split2 b =
-            split_q_one_scale(__fmul_rn(bf_lo(w[2 * e + 1]), qs.f), __fmul_rn(bf_hi(w[2 * e + 1]), qs.f));
-        hi[2 * h + e] = a.hi | (b.hi << 16);
-        lo[2 * h + e] = a.lo | (b.lo << 16);
-      }
-    }
-    const int o = swz16<D>(t, c);
-    *reinterpret_cast<uint4 *>(dst + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4 *>(dst + kRowsPerTile * D + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  for (int off = kLanes / 2; off >= 1; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+  const QScale qs = q_scale(top);
+  uint32_t hi[4], lo[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const Split2 a = split_q_one_scale(__fmul_rn(bf_lo(w[i]), qs.f), __fmul_rn(bf_hi(w[i]), qs.f));
+    hi[i] = a.hi;
+    lo[i] = a.lo;
   }
-  rowf[t] = __fmul_rn(p.cscale, qs.back);
+  __syncwarp();  // the row is read
+  const int o = swz16<D>(c, ch >> 1) + (ch & 1) * 8;
+  *reinterpret_cast<uint2 *>(dst + o) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+  *reinterpret_cast<uint2 *>(dst + kRowsPerTile * D + o) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+  if (ch == 0) rowf[c] = __fmul_rn(p.cscale, qs.back);
 }
 
 // An e4m3 V tile to fp16 (exact), 64-wide halves of 128-byte swizzled rows;
@@ -237,8 +290,7 @@ __global__ void __launch_bounds__(kR8Threads, 1)
     auto *start = reinterpret_cast<typename C::Start *>(smem + C::kOffH);
     Sched deal = strided_sched(p);
     if (p.sched) {
-      build_schedule<kRowsPerTile>(p, smem + C::kOffQ, C::kSchedScratch, start->sched_hist, start->sched_start,
-                                   start->sched_list, start->sched_meta, &start->sched_count);
+      build_schedule<kRowsPerTile>(p, smem + C::kOffQ, C::kSchedScratch, start->sched_hist, start->sched_list, start->sched_meta, &start->sched_count);
       if (start->sched_count >= 0) deal = Sched{start->sched_list, start->sched_meta, start->sched_count};
     }
     sc = Sched8{sm->units, min(deal.count, kSchedMaxMine)};
@@ -349,56 +401,68 @@ __global__ void __launch_bounds__(kR8Threads, 1)
     }
   } else if (warp >= C::kConv0) {
     // ------------------------------------------------------------------
-    // Converters: every V tile to fp16; a unit's query rows while the unit
-    // before it runs (after its second V tile).
+    // Converters: every V tile to fp16, and between a unit's first tiles the
+    // next unit's query rows, a few passes each (in one go, a thread per row,
+    // they held the V tiles up for 12000 cycles a unit).
     // ------------------------------------------------------------------
     regs_dec<kR8ConvRegs>();
+    constexpr int kAtOnce = 2;  // passes per tile
     const int t = threadIdx.x & 127;
     Unit cur, nxt;
-    int k = next_unit8(sc, 0, cur), gi = 0;
+    cur.n_tiles = 0;
+    int k = next_unit8(sc, 0, nxt), gi = 0;
     bool failed = false;
-    auto put_q = [&](const Unit &x, int ord) {
-      const int qb = ord & 1;
-      if (!mbar_wait(&sm->q_empty[qb], ((ord >> 1) & 1) ^ 1, abort_any, p.wait_ns)) return false;
-      convert_q_row<D>(p, x, t, smem + C::kOffQ + qb * C::kQBytes, sm->rowf[qb]);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm->q_full[qb]);
-      return true;
-    };
-    if (k >= 0) failed = !put_q(cur, 0);
-    for (int ui = 0; k >= 0 && !failed; ++ui) {
-      const int nk = next_unit8(sc, k + 1, nxt);
-      for (int j = 0; j < cur.n_tiles; ++j, ++gi) {
-        const int st = gi % NSV, sh = gi % NSH;
-        if (!mbar_wait(&sm->full_v[st], (gi / NSV) & 1, abort_any, p.wait_ns) ||
-            !mbar_wait(&sm->empty_h[sh], ((gi / NSH) & 1) ^ 1, abort_any, p.wait_ns)) {
-          failed = true;
-          break;
+    for (int ord = 0; !failed; ++ord) {  // nxt: the CTA's ord-th unit with tiles
+      uint8_t *qdst = smem + C::kOffQ + (ord & 1) * C::kQBytes;
+      int pass = k >= 0 ? -1 : kQPasses<D>;  // -1: its rows are not asked for yet
+      for (int j = 0; j < cur.n_tiles || pass < kQPasses<D>; ++j) {
+        bool ok = true;
+        if (j < cur.n_tiles) {
+          const int st = gi % NSV, sh = gi % NSH;
+          ok = mbar_wait(&sm->full_v[st], (gi / NSV) & 1, abort_any, p.wait_ns) &&
+               mbar_wait(&sm->empty_h[sh], ((gi / NSH) & 1) ^ 1, abort_any, p.wait_ns);
+          failed = !__all_sync(0xffffffffu, ok);  // (a warp goes on, or gives up, as one)
+          if (failed) break;
+          convert_v<D>(smem + C::kOffV + st * C::kKVBytes, smem + C::kOffH + sh * C::kHBytes,
+                       cur.lim_max - (cur.tok0 + j * kTileTokens), t);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&sm->full_h[sh]);
+            mbar_arrive(&sm->empty_v[st]);
+          }
+          ++gi;
         }
-        convert_v<D>(smem + C::kOffV + st * C::kKVBytes, smem + C::kOffH + sh * C::kHBytes,
-                     cur.lim_max - (cur.tok0 + j * kTileTokens), t);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sm->full_h[sh]);
-          mbar_arrive(&sm->empty_v[st]);
-        }
-        if (nk >= 0 && j == min(1, cur.n_tiles - 1) && !put_q(nxt, ui + 1)) {
-          failed = true;
-          break;
+        if (pass < 0) {
+          ok = mbar_wait(&sm->q_empty[ord & 1], ((ord >> 1) & 1) ^ 1, abort_any, p.wait_ns);
+          failed = !__all_sync(0xffffffffu, ok);
+          if (failed) break;
+          ask_q<D>(p, nxt, t, qdst);
+          pass = 0;
+        } else if (pass < kQPasses<D>) {
+          cp_async_wait<0>();
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < kAtOnce; ++e, ++pass) put_q_rows<D>(p, pass, t, qdst, sm->rowf[ord & 1]);
+          if (pass == kQPasses<D>) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm->q_full[ord & 1]);
+          }
         }
       }
+      if (k < 0) break;
       cur = nxt;
-      k = nk;
+      k = next_unit8(sc, k + 1, nxt);
     }
+    cp_async_wait<0>();
   } else if (warp < C::kEpi0) {
     // ------------------------------------------------------------------
     // Softmax warpgroups (see attn_rows.cuh for the exchange of the halves'
     // maxima and sums): thread t owns row t, warpgroup wg its keys [64 wg, 64
     // wg + 64).  O is rescaled half and half.
     // ------------------------------------------------------------------
-    regs_dec<kR8SoftmaxRegs>();
+    regs_inc<kR8SoftmaxRegs>();
     const int wg = warp >> 2, wq = warp & 3, t = threadIdx.x & 127;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t ocol = tmem + lane_off + C::kColO + wg * (D / 2);
@@ -571,40 +635,47 @@ __global__ void __launch_bounds__(kR8Threads, 1)
     // Epilogue warpgroup: thread t takes row t of each unit once its last P.V
     // is done, while the next unit's tiles already run.
     // ------------------------------------------------------------------
-    regs_inc<kR8EpiRegs>();
+    regs_dec<kR8EpiRegs>();
     const int wq = warp & 3, t = threadIdx.x & 127;
     const uint32_t orow = tmem + (static_cast<uint32_t>(wq * 32) << 16) + C::kColO;
     constexpr uint32_t bar_id = 3;
-    float acc[D];
     int uo = 0;
     for (int k = 0; k < sc.count; ++k) {
       const Unit x = sc.units[k];
       if (t == 0) check_sequence(p, x);
-      if (x.n_tiles == 0) {
-        // rows that see no key: out = 0, lse = -inf (by the unit of split 0)
-        if (x.s == 0 && t < x.rows) {
-#pragma unroll
-          for (int c = 0; c < D; ++c) acc[c] = 0.f;
-          write_final_row<D>(p, x, t, NEG_INF, 0.f, acc);
-        }
-        continue;
+      const bool any = x.n_tiles > 0;  // (without a tile: out = 0, lse = -inf, by the unit of split 0)
+      float m = NEG_INF, l = 0.f;
+      if (any) {
+        bool ok = mbar_wait(&sm->ml_full[uo & 1], (uo >> 1) & 1, abort_any, p.wait_ns);
+        m = sm->ml[uo & 1][0][t];
+        l = sm->ml[uo & 1][1][t];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm->ml_free[uo & 1]);
+        ok = mbar_wait(&sm->unit_done, uo & 1, abort_any, p.wait_ns) && ok;
+        if (wg_bar_or(bar_id, !ok)) break;
+        tc_fence_after_sync();
       }
-      bool ok = mbar_wait(&sm->ml_full[uo & 1], (uo >> 1) & 1, abort_any, p.wait_ns);
-      const float m_run = sm->ml[uo & 1][0][t], l_run = sm->ml[uo & 1][1][t];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm->ml_free[uo & 1]);
-      ok = mbar_wait(&sm->unit_done, uo & 1, abort_any, p.wait_ns) && ok;
-      if (wg_bar_or(bar_id, !ok)) break;
-      tc_fence_after_sync();
+      RowEnd r{};
+      if (t < x.rows && (any || x.s == 0)) r = row_end(p, x, t, m, l, D);
+#pragma unroll 1
+      for (int c = 0; c < D; c += 16) {
+        float v[16];
+        __syncwarp();
+        if (any) {
+          tmem_ld16(orow + c, v);
+          tmem_ld_wait_for(v);
+        } else {
 #pragma unroll
-      for (int ch = 0; ch < D / 16; ++ch) tmem_ld16(orow + ch * 16, *reinterpret_cast<float(*)[16]>(&acc[ch * 16]));
-#pragma unroll
-      for (int ch = 0; ch < D / 16; ++ch) tmem_ld_wait_for(*reinterpret_cast<float(*)[16]>(&acc[ch * 16]));
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm->o_free);
-      ++uo;
-      if (t < x.rows) finish_row_q8<D>(p, x, t, m_run, l_run, acc);
+          for (int e = 0; e < 16; ++e) v[e] = 0.f;
+        }
+        end_cols(p, r, c, v);
+      }
+      if (any) {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm->o_free);
+        ++uo;
+      }
     }
   }
 

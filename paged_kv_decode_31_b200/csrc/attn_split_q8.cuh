@@ -122,7 +122,7 @@ struct Q8Cfg {
     int sched_list[kSchedMaxMine];
     int sched_meta[kSchedMaxMine][3];
     Unit units[kSchedMaxMine];             // this CTA's units, worked out once
-    int sched_hist[kSchedHist], sched_start[kSchedBuckets];
+    int sched_hist[kSchedHist];
     int sched_count;
     __align__(16) int lim[kNW][N];         // [softmax warpgroup][row]: key limit
     int tab[kUS][kSplitTokens / 16];       // [unit % kUS]: block-table entries
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(32 * Q8Cfg<D, N, NSK, NSV>::kWarps, 1)
   {
     Sched deal = strided_sched(p);
     if (p.sched) {
-      build_schedule<N>(p, smem + C::kOffQ, C::kSchedScratch, sm->sched_hist, sm->sched_start,
+      build_schedule<N>(p, smem + C::kOffQ, C::kSchedScratch, sm->sched_hist,
                         sm->sched_list, sm->sched_meta, &sm->sched_count);
       if (sm->sched_count >= 0) deal = Sched{sm->sched_list, sm->sched_meta, sm->sched_count};
     }

@@ -90,7 +90,7 @@ int launch_split_q8(const Q8Params &p, const CUtensorMap &mk, const CUtensorMap 
   }
   const int grid = q8_grid(p, dev);
   Q8Params pp = p;
-  pp.sched = p.n_units <= C::kSchedScratch ? 1 : 0;
+  pp.sched = p.n_units > grid && p.n_units <= C::kSchedScratch ? 1 : 0;  // (one unit each: nothing to deal)
   kern<<<grid, 32 * C::kWarps, C::kSmemBytes, s>>>(pp, mk, mv);
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
@@ -126,7 +126,7 @@ int launch_rows_q8(const Q8Params &p, const CUtensorMap &mk, const CUtensorMap &
   }
   const int grid = q8_grid(p, dev);
   Q8Params pp = p;
-  pp.sched = p.n_units <= C::kSchedScratch ? 1 : 0;
+  pp.sched = p.n_units > grid && p.n_units <= C::kSchedScratch ? 1 : 0;  // (one unit each: nothing to deal)
   kern<<<grid, kR8Threads, C::kSmemBytes, s>>>(pp, mk, mv);
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
