@@ -160,10 +160,10 @@ __device__ __forceinline__ void end_cols(const Q8Params &p, const RowEnd &r, int
 // Query rows of unit x as q_hi and q_lo, by the converter warpgroup, in place:
 // the two halves of a row's bytes are copied to where its hi and its lo go
 // (ask_q, asynchronous), then the D / 8 lanes that share a row read it and
-// write both (put_q_pass: 1024 / D rows).  Rows past x.rows keep what the
+// write both (put_q_rows: kQRows rows).  Rows past x.rows keep what the
 // buffer holds: their S is not used.
 template <int D>
-constexpr int kQPasses = kRowsPerTile * (D / 8) / 128;
+constexpr int kQRows = 1024 / D;
 
 template <int D>
 __device__ __forceinline__ int raw_q_off(int r, int ch) {
@@ -414,8 +414,10 @@ __global__ void __launch_bounds__(kR8Threads, 1)
     bool failed = false;
     for (int ord = 0; !failed; ++ord) {  // nxt: the CTA's ord-th unit with tiles
       uint8_t *qdst = smem + C::kOffQ + (ord & 1) * C::kQBytes;
-      int pass = k >= 0 ? -1 : kQPasses<D>;  // -1: its rows are not asked for yet
-      for (int j = 0; j < cur.n_tiles || pass < kQPasses<D>; ++j) {
+      // passes over its rows; -1: they are not asked for yet
+      const int passes = k >= 0 ? (nxt.rows + kAtOnce * kQRows<D> - 1) / (kAtOnce * kQRows<D>) * kAtOnce : 0;
+      int pass = k >= 0 ? -1 : 0;
+      for (int j = 0; j < cur.n_tiles || pass < passes; ++j) {
         bool ok = true;
         if (j < cur.n_tiles) {
           const int st = gi % NSV, sh = gi % NSH;
@@ -439,12 +441,12 @@ __global__ void __launch_bounds__(kR8Threads, 1)
           if (failed) break;
           ask_q<D>(p, nxt, t, qdst);
           pass = 0;
-        } else if (pass < kQPasses<D>) {
+        } else if (pass < passes) {
           cp_async_wait<0>();
           __syncwarp();
 #pragma unroll
           for (int e = 0; e < kAtOnce; ++e, ++pass) put_q_rows<D>(p, pass, t, qdst, sm->rowf[ord & 1]);
-          if (pass == kQPasses<D>) {
+          if (pass == passes) {
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm->q_full[ord & 1]);
@@ -483,6 +485,7 @@ __global__ void __launch_bounds__(kR8Threads, 1)
       const float rf = t < x.rows ? sm->rowf[uo & 1][t] : 1.f;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm->q_empty[uo & 1]);
+      const bool live = 32 * wq < x.rows;  // (a warp without rows leaves its S and O as they are)
       float m_run = NEG_INF, l_run = 0.f;
       float a_prev = 1.f, half_prev = 0.f;
       for (int j = 0; j < x.n_tiles; ++j) {
@@ -511,7 +514,7 @@ __global__ void __launch_bounds__(kR8Threads, 1)
         const bool full = __all_sync(0xffffffffu, nvis == kTileTokens);  // warp-uniform
         float hm = NEG_INF;
 #pragma unroll 1
-        for (int q = 0; q < 4; q += 2) {
+        for (int q = live ? 0 : 4; q < 4; q += 2) {
           float v0[16], v1[16];
           tmem_ld16(srow + 64 * wg + 16 * q, v0);
           tmem_ld16(srow + 64 * wg + 16 * q + 16, v1);
@@ -567,7 +570,7 @@ __global__ void __launch_bounds__(kR8Threads, 1)
         // pass 2: P over S, and this half's sum of P 2^-ev
         float half = 0.f;
 #pragma unroll 1
-        for (int g2 = 0; g2 < 2; ++g2) {  // 32 keys
+        for (int g2 = live ? 0 : 2; g2 < 2; ++g2) {  // 32 keys
           float v[2][16];
           tmem_ld16(srow + 64 * wg + 32 * g2, v[0]);
           tmem_ld16(srow + 64 * wg + 32 * g2 + 16, v[1]);
@@ -658,7 +661,7 @@ __global__ void __launch_bounds__(kR8Threads, 1)
       RowEnd r{};
       if (t < x.rows && (any || x.s == 0)) r = row_end(p, x, t, m, l, D);
 #pragma unroll 1
-      for (int c = 0; c < D; c += 16) {
+      for (int c = 32 * wq < x.rows ? 0 : D; c < D; c += 16) {
         float v[16];
         __syncwarp();
         if (any) {
