@@ -454,7 +454,7 @@ int pkv_rope(const void *q, const int64_t q_strides[3], void *q_out, const int64
  * otherwise packed, [total_new, heads, D] with the last two of the strides
  * used, sequence b owning cu_seqlens_new[b] .. cu_seqlens_new[b+1] - 1.  Tokens
  * behind cu_seqlens_new[batch] are left alone.  Two sequences must not share a
- * block that the call writes.  Errors and device error bits as pkv_kv_append;
+ * block that the call writes, nor may a table name one twice there.  Errors and device error bits as pkv_kv_append;
  * a range of cu_seqlens_new that decreases or leaves [0, total_new] sets
  * PKV_DEVERR_QUERY_LEN and is skipped.
  */
@@ -519,12 +519,19 @@ int pkv_kv_append_q8(const void *q, const int64_t q_strides[3], void *q_out, con
  * an 8-bit cache: the same arguments with the scale views behind the caches,
  * the same workspace (pkv_workspace_size, pkv_varlen_workspace_size), masks,
  * errors and error bits (and PKV_DEVERR_SCALE), the same splits and merge.  0 <
- * scale <= 8.  q stays bf16 and out bf16: a query row takes part as two 8-bit
- * operands that add up to it (to 2^-21 of its largest element or exactly; rows
- * whose largest magnitude is above 2^67 saturate), a probability as three that
- * add up to its fp16 value; sums and softmax statistics are fp32.  For a given
- * cache a row's bits depend on its own query and keys alone: not on the batch,
- * the table, or which of the three calls computed it.
+ * scale <= 8.  q stays bf16 and out bf16; sums and softmax statistics are
+ * fp32.  A query row takes part as two 8-bit operands that add up to it (to
+ * 2^-21 of its largest element or exactly; rows whose largest magnitude is
+ * above 2^67 saturate), a probability rounded to fp16 (as three 8-bit operands
+ * that add up to that, or as one fp16 operand).
+ * A request of n query tokens with n * Hq / Hkv <= 16 rows per KV head is
+ * computed by one kernel, larger ones by another (their sums round in another
+ * order); in a packed call each request's own n decides.  Within either, for a
+ * given cache, a row's bits depend on its own query and keys alone: not on the
+ * other requests, the table, or which of the three calls computed it.  K and V
+ * must be finite for the tokens of a request that any of
+ * its rows sees: a NaN in a value reaches the rows computed with it, those that
+ * do not see its token too.  Slots behind a sequence may hold anything.
  */
 int pkv_paged_decode_attn_q8(const void *q, const int64_t q_strides[3], const void *k_cache,
                              const int64_t k_strides[3], const void *v_cache,
