@@ -529,9 +529,10 @@ int pkv_kv_append_q8(const void *q, const int64_t q_strides[3], void *q_out, con
  * order); in a packed call each request's own n decides.  Within either, for a
  * given cache, a row's bits depend on its own query and keys alone: not on the
  * other requests, the table, or which of the three calls computed it.  K and V
- * must be finite for the tokens of a request that any of
- * its rows sees: a NaN in a value reaches the rows computed with it, those that
- * do not see its token too.  Slots behind a sequence may hold anything.
+ * must be finite for the tokens of a request that any of its rows sees: a NaN
+ * in a value reaches the rows computed with it, those that do not see its token
+ * too.  A query row that is not finite has no defined result and leaves the
+ * others alone.  Slots behind a sequence may hold anything.
  */
 int pkv_paged_decode_attn_q8(const void *q, const int64_t q_strides[3], const void *k_cache,
                              const int64_t k_strides[3], const void *v_cache,

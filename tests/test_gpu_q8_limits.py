@@ -141,3 +141,42 @@ def test_slices_of_one_projection_and_stream_handles():
         got.append((x, *(t.view(torch.uint8) for t in dev), out, lse))
     for other in got[1:]:
         assert all(torch.equal(a, b) for a, b in zip(got[0], other))
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,n", [(128, 8, 2, [3, 40, 1]), (64, 3, 1, [50, 2, 7])])
+def test_unaligned_outputs(D, Hq, Hkv, n):
+    """out and the final rows with strides that no 16-byte store fits: the same
+    bits, in both kernels, with one split and two, and nothing beside them."""
+    gen = torch.Generator().manual_seed(D)
+    lens = [n[0] + 30, 4200, n[2]]
+    table, blocks = Q.table_for(lens, 16, gen)
+    dev = Q.cuda_cache(*Q.make_cache8(blocks, 16, Hkv, D, gen, 2))
+    q = _bf16((sum(n), Hq, D), gen).cuda()
+    cu = torch.tensor([0] + torch.tensor(n).cumsum(0).tolist(), dtype=torch.int32).cuda()
+    a = (q, *dev, table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), cu, max(n))
+    for msk in (4200, 9000):
+        want = pkv.paged_varlen_attn_q8(*a, max_seqlen_k=msk, final=True)
+        wide = torch.full((sum(n), Hq, D + 3), 7.0, dtype=torch.bfloat16, device="cuda")
+        last = torch.full((3, Hq, D + 1), 7.0, dtype=torch.bfloat16, device="cuda")
+        got = pkv.paged_varlen_attn_q8(*a, max_seqlen_k=msk, out=wide[..., 1:D + 1], final_out=last[..., 1:])
+        for x, y in zip(want, got):
+            assert torch.equal(x, y)
+        assert torch.all(wide[..., 0] == 7.0) and torch.all(wide[..., D + 1:] == 7.0) and torch.all(last[..., 0] == 7.0)
+
+
+@pytest.mark.parametrize("sq", [2, 40])
+def test_a_query_row_that_is_not_finite_leaves_the_others_alone(sq):
+    gen = torch.Generator().manual_seed(sq)
+    kc, vc, ks, vs = Q.make_cache8(8, 16, 2, 128, gen, 3)
+    table = torch.randperm(8, generator=gen).to(torch.int32)[None].cuda()
+    a = (*Q.cuda_cache(kc, vc, ks, vs), table, torch.tensor([100], dtype=torch.int32, device="cuda"))
+    q = _bf16((1, sq, 8, 128), gen).cuda()
+    want = pkv.paged_prefill_attn_q8(q, *a)
+    bad = q.clone()
+    bad[0, 1, 3, 5] = float("nan")
+    bad[0, 0, 6, 9] = float("-inf")
+    got = pkv.paged_prefill_attn_q8(bad, *a)
+    same = torch.ones(1, sq, 8, dtype=torch.bool, device="cuda")
+    same[0, 1, 3] = same[0, 0, 6] = False
+    assert torch.equal(want[0][same], got[0][same])
+    assert torch.equal(want[1].transpose(1, 2)[same], got[1].transpose(1, 2)[same])
