@@ -180,3 +180,32 @@ def test_a_query_row_that_is_not_finite_leaves_the_others_alone(sq):
     same[0, 1, 3] = same[0, 0, 6] = False
     assert torch.equal(want[0][same], got[0][same])
     assert torch.equal(want[1].transpose(1, 2)[same], got[1].transpose(1, 2)[same])
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 24, 1), (64, 32, 2), (128, 17, 1), (64, 40, 5)])
+def test_packed_requests_of_many_heads(D, Hq, Hkv):
+    """More than 16 query heads per KV head (every request in the row-major
+    kernel), exactly 16, and 8: packed equals the request alone, both within the
+    bounds of the exact result; a decode step among prompts."""
+    gen = torch.Generator().manual_seed(Hq)
+    n, lens = [1, 0, 2, 19, 1, 1], [300, 7, 2, 140, 0, 4100]
+    table, blocks = Q.table_for(lens, 64, gen)
+    kc, vc, ks, vs = Q.make_cache8(blocks, 64, Hkv, D, gen, 3)
+    dev = Q.cuda_cache(kc, vc, ks, vs)
+    q = _bf16((sum(n), Hq, D), gen)
+    cu = torch.tensor([0] + torch.tensor(n).cumsum(0).tolist(), dtype=torch.int32)
+    sl = torch.tensor(lens, dtype=torch.int32)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse, fo, fl = pkv.paged_varlen_attn_q8(q.cuda(), *dev, table.cuda(), sl.cuda(), cu.cuda(), max(n),
+                                                max_seqlen_k=4100, final=True, err=err)
+    assert int(err) == 0
+    for b, k in enumerate(n):
+        if not k:
+            continue
+        a, one = int(cu[b]), slice(b, b + 1)
+        qb = q[a:a + k][None]
+        o, l = pkv.paged_decode_attn_q8(qb.cuda(), *dev, table[one].cuda(), sl[one].cuda(), max_seqlen_k=4100,
+                                        causal=True)
+        assert torch.equal(o[0], out[a:a + k]) and torch.equal(l[0], lse[:, a:a + k])
+        assert torch.equal(fo[b], out[a + k - 1]) and torch.equal(fl[b], lse[:, a + k - 1])
+        Q.check_attention(o, l, *Q.attention(qb, kc, vc, ks, vs, table[one], sl[one], D ** -0.5, True))
