@@ -708,6 +708,9 @@ __global__ void __launch_bounds__(kR8Threads, 1)
     tmem_dealloc(tmem, 512);
   }
   if (threadIdx.x == 0 && sm->abort_any && p.err) atomicOr(p.err, kErrTimeout);
+  // (a grid that overlaps the decode kernel's before it ends after it, so what
+  // follows on the stream finds both complete)
+  wait_for_grids_before();
 }
 
 }  // namespace pkv

@@ -482,6 +482,9 @@ __global__ void __launch_bounds__(32 * Q8Cfg<D, N, NSK, NSV>::kWarps, 1)
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
+  // In a packed call the row-major kernel's CTAs take the SMs over as this
+  // grid's leave them (every CTA of it is resident or has been by now).
+  if (threadIdx.x == 0) launch_dependents();
   const uint32_t tmem = sm->tmem_base;
   const uint32_t sbase = smem_u32(smem);
   // the Q and P^T buffers are not in use yet: the schedule's scratch

@@ -110,7 +110,8 @@ int launch_split_q8_rows(int64_t rows, const Q8Params &p, const CUtensorMap &mk,
 // The row-major kernel shares out its registers between warpgroups; the
 // launch is refused if the build differs from what the shares add up to.
 template <int D>
-int launch_rows_q8(const Q8Params &p, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t s, int dev) {
+int launch_rows_q8(const Q8Params &p, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t s, int dev,
+                   bool overlap) {
   using C = R8Cfg<D>;
   static_assert(C::kSmemBytes <= 232448, "shared memory budget");
   static std::atomic<bool> attr_set[kMaxDevices];
@@ -127,8 +128,19 @@ int launch_rows_q8(const Q8Params &p, const CUtensorMap &mk, const CUtensorMap &
   const int grid = q8_grid(p, dev);
   Q8Params pp = p;
   pp.sched = p.n_units > grid && p.n_units <= C::kSchedScratch ? 1 : 0;  // (one unit each: nothing to deal)
-  kern<<<grid, kR8Threads, C::kSmemBytes, s>>>(pp, mk, mv);
-  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kR8Threads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = overlap ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, pp, mk, mv) == cudaSuccess && cudaGetLastError() == cudaSuccess
+             ? PKV_OK
+             : PKV_ERR_CUDA;
 }
 
 // Rows per KV head up to which a request is served by the split kernel (one
@@ -272,8 +284,8 @@ int attn_q8_entry(const void *q, const int64_t q_strides[3], const void *k_cache
     p.nq_lo = small_nq + 1;
   }
   rc = split_only ? launch_split_q8_rows(R, p, mk, mv, D, s, dev)
-       : D == 128 ? launch_rows_q8<128>(p, mk, mv, s, dev)
-                  : launch_rows_q8<64>(p, mk, mv, s, dev);
+       : D == 128 ? launch_rows_q8<128>(p, mk, mv, s, dev, both)
+                  : launch_rows_q8<64>(p, mk, mv, s, dev, both);
   if (rc != PKV_OK || p.direct) return rc;
 
   MergeParams m{};

@@ -377,6 +377,13 @@ __device__ __forceinline__ void tmem_ld_wait_for8(float *v) {
 
 // Each thread of the warp writes 16 consecutive 32-bit columns of its own
 // TMEM lane (the mirror of tmem_ld16).
+// Programmatic dependent launch.  launch_dependents: a grid launched to overlap
+// this one may start once every CTA of this grid has got here (or ended).
+// wait: the grids before this one are complete and their writes visible; at
+// once in a grid that was launched in plain stream order.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_grids_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
