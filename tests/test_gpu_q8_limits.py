@@ -209,3 +209,47 @@ def test_packed_requests_of_many_heads(D, Hq, Hkv):
         assert torch.equal(o[0], out[a:a + k]) and torch.equal(l[0], lse[:, a:a + k])
         assert torch.equal(fo[b], out[a + k - 1]) and torch.equal(fl[b], lse[:, a + k - 1])
         Q.check_attention(o, l, *Q.attention(qb, kc, vc, ks, vs, table[one], sl[one], D ** -0.5, True))
+
+
+def test_packed_calls_one_after_another_and_captured():
+    """The two launches of a packed call overlap at their ends: an append before
+    the call is seen by both, what follows sees both complete, and a captured
+    sequence of steps replays to the same bits."""
+    gen = torch.Generator().manual_seed(31)
+    Hq, Hkv, D, bs = 16, 4, 128, 16
+    n, before = [1, 1, 2, 200, 1, 90], [4000, 900, 50, 700, 5000, 0]
+    table, blocks = Q.table_for([b + 4 * k for b, k in zip(before, n)], bs, gen)
+    cache = Q.make_cache8(blocks, bs, Hkv, D, gen, 2)
+    cu = torch.tensor([0] + torch.tensor(n).cumsum(0).tolist(), dtype=torch.int32).cuda()
+    table, step = table.cuda(), (cu[1:] - cu[:-1]).contiguous()
+    f = pkv.rope_frequencies(D, device="cuda")[0]
+    new = [[_bf16((sum(n), h, D), gen).cuda() for h in (Hq, Hkv, Hkv)] for _ in range(4)]
+
+    def steps(dev, sl, wait):
+        outs = []
+        for q, k, v in new:
+            q = pkv.kv_append_q8(k, v, *dev, table, sl, q=q, inv_freq=f, cu_seqlens_new=cu)
+            if wait:
+                torch.cuda.synchronize()
+            sl = sl + step
+            o, l = pkv.paged_varlen_attn_q8(q, *dev, table, sl, cu, max(n), max_seqlen_k=6000)
+            outs += [o.clone(), l.clone()]  # (reads both launches' rows at once)
+            if wait:
+                torch.cuda.synchronize()
+        return outs
+
+    start = torch.tensor(before, dtype=torch.int32).cuda()
+    want = steps(Q.cuda_cache(*cache), start, True)
+    got = steps(Q.cuda_cache(*cache), start, False)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    dev, fresh = Q.cuda_cache(*cache), Q.cuda_cache(*cache)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = steps(dev, start, False)
+    for _ in range(2):
+        for a, b in zip(dev, fresh):
+            a.view(torch.uint8).copy_(b.view(torch.uint8))
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
