@@ -332,7 +332,8 @@ __device__ __forceinline__ void prepare_q8(const Q8Params &p, uint8_t *smem, typ
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm->tab_full[ui % US]);
     // Q goes into the buffer of the unit two before this one, once that unit's
-    // last QK^T and its epilogue (staged there) are done
+    // last QK^T and its epilogue (staged there) are done and the softmax warps
+    // have seen it
     if (!wait(&sm->q_empty[ui % QB], ((ui / QB) & 1) ^ 1)) break;
     cp_async_wait<1>();
     __syncwarp();
@@ -472,7 +473,8 @@ __global__ void __launch_bounds__(32 * Q8Cfg<D, N, NSK, NSV>::kWarps, 1)
       mbar_init(&sm->unit_done[i], 1);
       mbar_init(&sm->o_free[i], 4);   // one arrival per correction warp
       mbar_init(&sm->q_full[i], 1);
-      mbar_init(&sm->q_empty[i], 2);  // the unit's last QK^T, and its epilogue
+      // the unit's last QK^T, its epilogue, and every softmax warp
+      mbar_init(&sm->q_empty[i], 2 + 4 * C::kNW);
       mbar_init(&sm->drain[i], 1);
     }
     sm->abort_any = 0;
@@ -622,8 +624,9 @@ __global__ void __launch_bounds__(32 * Q8Cfg<D, N, NSK, NSV>::kWarps, 1)
         }
         sm->lim[wg][t] = lim;
       }
-      // the unit's Q and row factors are staged (the buffer is not filled
-      // again before this unit's epilogue, so the phase cannot move on)
+      // the unit's Q and row factors are staged.  (A warpgroup without a pair in
+      // the unit waits too, and the unit's end does not wait for it: what keeps
+      // the phase from moving on past it is its own arrival at q_empty below.)
       const bool okq = mbar_wait_call(&sm->q_full[uo % QB], (uo / QB) & 1, abort_any, p.wait_ns);
       const float *rowf = sm->rowf[uo % QB];
       if (wg_bar_or(bar_id, !okq)) {
@@ -814,6 +817,10 @@ __global__ void __launch_bounds__(32 * Q8Cfg<D, N, NSK, NSV>::kWarps, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm->p_full[bb]);
       }
+      if (stop) break;
+      // this warp is through with the unit's Q buffer: its phase, its row factors
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm->q_empty[uo % QB]);
       gbase += x.n_tiles;
       pbase += (x.n_tiles + 1) >> 1;
       ++uo;
