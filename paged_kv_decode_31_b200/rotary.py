@@ -62,7 +62,9 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: Optiona
             # pair index at which f_i turns n times within original_max
             at = [half * math.log(original_max / (2 * math.pi * n)) / math.log(base)
                   for n in (fast, slow)]
-            lo, hi = max(math.floor(at[0]), 0), min(math.ceil(at[1]), half - 1)
+            # whole indexes, held to [0, rotary_dim - 1]: the upper border may lie
+            # past the last pair, which then keeps a part of its frequency
+            lo, hi = max(math.floor(at[0]), 0), min(math.ceil(at[1]), rotary_dim - 1)
             keep = 1 - ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
             m = 0.1 * math.log(factor) + 1.0
         f = f * keep + f / factor * (1 - keep)
