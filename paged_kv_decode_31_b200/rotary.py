@@ -65,7 +65,8 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: Optiona
             # whole indexes, held to [0, rotary_dim - 1]: the upper border may lie
             # past the last pair, which then keeps a part of its frequency
             lo, hi = max(math.floor(at[0]), 0), min(math.ceil(at[1]), rotary_dim - 1)
-            keep = 1 - ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+            # (hi <= 0: not even the fastest pair turns more than `slow` times)
+            keep = 1 - ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1) if hi > 0 else torch.zeros_like(i)
             m = 0.1 * math.log(factor) + 1.0
         f = f * keep + f / factor * (1 - keep)
     elif scaling not in (None, "base"):

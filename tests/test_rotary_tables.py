@@ -51,3 +51,10 @@ def test_blend_where_the_last_pair_still_turns():
     f, _ = pkv.rope_frequencies(128, scaling="blend", factor=4.0, original_max=131072)
     plain, _ = pkv.rope_frequencies(128)
     assert 0.4 < float(f[-1] / plain[-1]) < 0.5
+
+
+def test_blend_where_no_pair_turns():
+    """A trained length within one turn of the fastest pair: all are stretched."""
+    f, _ = pkv.rope_frequencies(32, scaling="blend", factor=4.0, original_max=5)
+    plain, _ = pkv.rope_frequencies(32)
+    assert torch.equal(f, plain / 4)
