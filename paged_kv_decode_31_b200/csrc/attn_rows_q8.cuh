@@ -11,9 +11,9 @@
 //   w   = S (c 2^-k 2^ek) + ev per key (see attn_split_q8.cuh): the exponents
 //         are those of a 16-key group at least, so a group's largest score
 //         alone goes through the fused multiply-add to give its largest w;
-//   m     rises to max(w) when that exceeds it by more than kMaxSlack;
-//   P   = fp16(2^(w - m)) <= 2^8 (off by at most 2^-11 relative, 2^-25
-//         absolute) over S in TMEM;
+//   m     rises to max(w) - kRowDrop when max(w) > m + kRefTop;
+//   P   = fp16(2^(w - m)) <= 2^15 (off by at most 2^-11 relative, 2^-25
+//         absolute, which is 2^-32 of a row's largest) over S in TMEM;
 //   O  += P V16 (kind::f16), V16 the tile's e4m3 values as fp16, exactly;
 //   l   = sum of 2^(w - m) 2^-ev in fp32, group sums first.
 // Against the bf16 kernel, P is one operand where that takes two (an fp16 has
@@ -46,6 +46,9 @@
 namespace pkv {
 
 constexpr int kR8Threads = 640;
+// A row's largest P stays in [2^kRowDrop, 2^kRefTop] (see attn_split_q8.cuh):
+// with [2^0, 2^8] the tokens 14 nats below it kept 4 bits of fp16 and fewer.
+constexpr float kRowDrop = 7.f;
 // Registers per thread: at launch, and each warpgroup's share of their sum.
 constexpr int kR8LaunchRegs = 96, kR8SoftmaxRegs = 128, kR8EpiRegs = 88, kR8ConvRegs = 72, kR8AuxRegs = 64;
 static_assert(2 * kR8SoftmaxRegs + kR8EpiRegs + kR8ConvRegs + kR8AuxRegs == 5 * kR8LaunchRegs,
@@ -565,7 +568,7 @@ __global__ void __launch_bounds__(kR8Threads, 1)
           l_run = __fmaf_rn(l_run, a_prev, __fadd_rn(half_prev, sm->xsum[(gi - 1) & 1][t]));
         const float mx = fmaxf(hm, sm->xmax[gi & 1][wg ^ 1][t]);
         const float m_prev = m_run;
-        const float m_new = (mx > __fadd_rn(m_prev, kMaxSlack)) ? mx : m_prev;
+        const float m_new = (mx > __fadd_rn(m_prev, kRefTop)) ? __fsub_rn(mx, kRowDrop) : m_prev;
         m_run = m_new;
         const float a = (m_prev == NEG_INF || m_new == m_prev) ? 1.f : ex2(__fsub_rn(m_prev, m_new));
         if (__any_sync(0xffffffffu, a != 1.f)) {

@@ -16,8 +16,8 @@
 //   each: the chain of reductions, barriers and fences is latency, and its
 //   length hardly depends on how much it carries)
 //   m     the row's running reference (-inf at the split's start) rises to
-//           max(w) - kRefDrop when max(w) > m + 8; P = 2^(w - m) is then at
-//           most 2^8 and at least 2^(8 - kRefSlack) for the largest token;
+//           max(w) - kRefDrop when max(w) > m + kRefTop; P = 2^(w - m) is then
+//           at most 2^kRefTop and at least 2^kRefDrop for the largest token;
 //   O^T  += V8^T * [P_hi | P_mid | P_lo]^T, P as three 8-bit operands side by
 //           side (split_p), joined (join_p) at the split's end;
 //   l     = sum of 2^(w - ev - m) = P 2^-ev over the tokens, in fp32.
@@ -43,13 +43,14 @@
 
 namespace pkv {
 
-// P <= 2^8 fits e4m3 (448); the reference moves when the largest token passes
-// it, and then to 2^kRefDrop below that token, so a row's largest P stays in
-// [2^kRefDrop, 2^8] (p's smallest step, 2^-18, is then at most 2^-20 of it).
-// Each move waits for the P.V under way and rescales O, 6000 cycles without a
-// new tile: with 6 for kRefDrop moves in the first tiles of every split cost a
-// third of the time.
-constexpr float kRefTop = 8.f, kRefDrop = 2.f;
+// P <= 2^15 fits fp16 and e5m2 with room for the pieces' factors; the reference
+// moves when the largest token passes it, and then to 2^kRefDrop below that
+// token, so a row's largest P stays in [2^kRefDrop, 2^kRefTop] and the rounding
+// of the smallest, 2^-25, is at most 2^-34 of it: less than fp32's own over a
+// split's 4096 tokens.  Each move waits for the P.V under way and rescales O,
+// 6000 cycles without a new tile: with a distance of 2 between the two, moves
+// in the first tiles of every split cost a third of the time.
+constexpr float kRefTop = 15.f, kRefDrop = 9.f;
 
 struct Q8Params : AttnParams {
   const uint8_t *k_sc, *v_sc;  // scale bytes of (block, KV head)
@@ -524,7 +525,7 @@ __global__ void __launch_bounds__(32 * Q8Cfg<D, N, NSK, NSV>::kWarps, 1)
       const bool is_qk = warp == C::kQkW;
       // A = K tile, B = [q_hi | q_lo] (K-major); A = V^T, B = P^T (MN-major)
       constexpr uint32_t kQk = idesc_f8(128, C::kQCols, kFmtE4M3, kFmtE4M3, 0, 0);
-      constexpr uint32_t kPv = idesc_f8(128, C::kPCols, kFmtE4M3, kFmtE4M3, 1, 1);
+      constexpr uint32_t kPv = idesc_f8(128, C::kPCols, kFmtE4M3, kFmtE5M2, 1, 1);
       int gi = 0, pi = 0, ui = 0;
       bool failed = false;
       for (int k = 0; k < sc.count && !failed; ++k) {

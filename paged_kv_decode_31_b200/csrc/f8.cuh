@@ -27,15 +27,20 @@ __device__ __forceinline__ uint32_t e4m3x2_of(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ uint32_t e4m3x2_of(__half2 v) {
+__device__ __forceinline__ uint32_t e5m2x2_of(__half2 v) {
   uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<uint32_t *>(&v)));
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<uint32_t *>(&v)));
   return r;
 }
-// Back to fp16: exact (every e4m3 value is an fp16 value).
+// Back to fp16: exact (every e4m3 or e5m2 value is an fp16 value).
 __device__ __forceinline__ __half2 half2_of_e4m3x2(uint32_t v) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(v)));
+  return *reinterpret_cast<__half2 *>(&r);
+}
+__device__ __forceinline__ __half2 half2_of_e5m2x2(uint32_t v) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(v)));
   return *reinterpret_cast<__half2 *>(&r);
 }
 // A query row enters K Q^T as two e4m3 operands whose products are accumulated
@@ -71,13 +76,17 @@ __device__ __forceinline__ Split2 split_q_one_scale(float x0, float x1) {
   return s;
 }
 
-// A probability in [0, 256], rounded to fp16 (11 bits: off by at most 2^-11
-// relative), enters P V as three e4m3 operands whose products are accumulated
-// apart and joined in fp32 as hi + (mid + lo / 16) / 16:
-//   hi = e4m3(p),  mid = e4m3(16 (p - hi)),  lo = e4m3(16 (16 (p - hi) - mid)).
-// The differences are exact in fp16, and hi and mid leave at most two units of
-// p's last bit to lo, so the three hold the fp16 value; small ones too, down
-// to half of lo's smallest step, 2^-18.
+// A probability in [0, 2^15], rounded to fp16 (11 bits: off by at most 2^-11
+// relative, 2^-25 where fp16 is subnormal), enters P V as three e5m2 operands
+// whose products are accumulated apart and joined in fp32 as hi + (mid + lo /
+// 16) / 16:
+//   hi = e5m2(p),  mid = e5m2(16 (p - hi)),  lo = e5m2(16 (16 (p - hi) - mid)).
+// The differences are exact in fp16.  e5m2 rounds to 3 bits, so of p's 11 bits
+// hi leaves at most 2^7 units of the last and mid at most 2^3, which lo holds:
+// the three are the fp16 value, the subnormal ones included (hi's smallest step
+// is 2^-16, lo's 2^-16 / 2^8 is fp16's).  (e4m3 pieces, with a bit more each but
+// 2^7 less range, lost every p below 2^-18 against a largest of 2^2 to 2^8:
+// with one token 12 to 15 nats above thousands of others, all of theirs.)
 struct SplitP {
   uint32_t hi, mid, lo;
 };
@@ -85,11 +94,11 @@ __device__ __forceinline__ SplitP split_p(float p0, float p1) {
   SplitP s;
   const __half2 k16 = __floats2half2_rn(16.f, 16.f);
   __half2 r = __floats2half2_rn(p0, p1);
-  s.hi = e4m3x2_of(r);
-  r = __hmul2(__hsub2(r, half2_of_e4m3x2(s.hi)), k16);
-  s.mid = e4m3x2_of(r);
-  r = __hmul2(__hsub2(r, half2_of_e4m3x2(s.mid)), k16);
-  s.lo = e4m3x2_of(r);
+  s.hi = e5m2x2_of(r);
+  r = __hmul2(__hsub2(r, half2_of_e5m2x2(s.hi)), k16);
+  s.mid = e5m2x2_of(r);
+  r = __hmul2(__hsub2(r, half2_of_e5m2x2(s.mid)), k16);
+  s.lo = e5m2x2_of(r);
   return s;
 }
 __device__ __forceinline__ float join_p(float hi, float mid, float lo) {
