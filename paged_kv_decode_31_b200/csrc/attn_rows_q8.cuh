@@ -15,7 +15,8 @@
 //   P   = fp16(2^(w - m)) <= 2^15 (off by at most 2^-11 relative, 2^-25
 //         absolute, which is 2^-32 of a row's largest) over S in TMEM;
 //   O  += P V16 (kind::f16), V16 the tile's e4m3 values as fp16, exactly;
-//   l   = sum of 2^(w - m) 2^-ev in fp32, group sums first.
+//   l   = sum of 2^(w - m) 2^-ev in fp32, group sums first; a move of m scales
+//         it in two steps (see attn_split_q8.cuh).
 // Against the bf16 kernel, P is one operand where that takes two (an fp16 has
 // the bits that a bf16 and its remainder are there for), so P.V is half the
 // products, the softmax stores half the bytes and O is one accumulator, which
@@ -40,6 +41,8 @@
 // 18 MMA issuer + TMEM owner, 19 the units' tables and scales.
 #pragma once
 
+#include <type_traits>
+
 #include "attn_rows.cuh"
 #include "attn_split_q8.cuh"
 
@@ -49,6 +52,14 @@ constexpr int kR8Threads = 640;
 // A row's largest P stays in [2^kRowDrop, 2^kRefTop] (see attn_split_q8.cuh):
 // with [2^0, 2^8] the tokens 14 nats below it kept 4 bits of fp16 and fewer.
 constexpr float kRowDrop = 7.f;
+// P is flushed to zero below 2^-126, which must not take its P 2^-ev out of l:
+// groups of keys with a scale below 2^kRowEvMin (blocks of zeros have 2^-63) go
+// through the exponential with 2^kRowEvMin in its place, and P gets the rest
+// afterwards.  What is flushed then is below 2^-102 of l's units, 2^-90 for a
+// split's 4096 tokens, and l at least 2^(kRowDrop - 63).  (The form of
+// attn_split_q8.cuh costs a product per element here, issue slots that this
+// kernel does not have: 146 us instead of 139.6 for 8 x 512 queries.)
+constexpr float kRowEvMin = -24.f;
 // Registers per thread: at launch, and each warpgroup's share of their sum.
 constexpr int kR8LaunchRegs = 96, kR8SoftmaxRegs = 128, kR8EpiRegs = 88, kR8ConvRegs = 72, kR8AuxRegs = 64;
 static_assert(2 * kR8SoftmaxRegs + kR8EpiRegs + kR8ConvRegs + kR8AuxRegs == 5 * kR8LaunchRegs,
@@ -509,7 +520,7 @@ __global__ void __launch_bounds__(kR8Threads, 1)
       if (lane == 0) mbar_arrive(&sm->q_empty[uo & 1]);
       const bool live = 32 * wq < x.rows;  // (a warp without rows leaves its S and O as they are)
       float m_run = NEG_INF, l_run = 0.f;
-      float a_prev = 1.f, half_prev = 0.f;
+      float root_prev = 1.f, half_prev = 0.f;
       for (int j = 0; j < x.n_tiles; ++j) {
         const int gi = gbase + j, bb = gi % SB, sl = gi % C::kSC;
         bool ok = mbar_wait(&sm->sc_full[sl], (gi / C::kSC) & 1, abort_any, p.wait_ns) && okq;
@@ -527,7 +538,7 @@ __global__ void __launch_bounds__(kR8Threads, 1)
           const int both = tok0 + key < x.lim_max ? sm->sc[sl][key >> p.box_shift] : 127 | (127 << 8);
           f[q] = __fmul_rn(rf, scale_of(both & 255));
           ev[q] = static_cast<float>((both >> 8) - 127);
-          iv[q] = inv_scale_of(both >> 8);
+          iv[q] = inv_scale_of(max(both >> 8, 127 + static_cast<int>(kRowEvMin)));
         }
         // pass 1: this half's largest w (the fused multiply-add rounds
         // monotonically, so a group's largest score gives its largest w).
@@ -565,13 +576,16 @@ __global__ void __launch_bounds__(kR8Threads, 1)
           break;
         }
         if (wg == 0 && j > 0)
-          l_run = __fmaf_rn(l_run, a_prev, __fadd_rn(half_prev, sm->xsum[(gi - 1) & 1][t]));
+          l_run = __fmaf_rn(__fmul_rn(l_run, root_prev), root_prev, __fadd_rn(half_prev, sm->xsum[(gi - 1) & 1][t]));
         const float mx = fmaxf(hm, sm->xmax[gi & 1][wg ^ 1][t]);
         const float m_prev = m_run;
         const float m_new = (mx > __fadd_rn(m_prev, kRefTop)) ? __fsub_rn(mx, kRowDrop) : m_prev;
         m_run = m_new;
-        const float a = (m_prev == NEG_INF || m_new == m_prev) ? 1.f : ex2(__fsub_rn(m_prev, m_new));
-        if (__any_sync(0xffffffffu, a != 1.f)) {
+        const float d = (m_prev == NEG_INF || m_new == m_prev) ? 0.f : __fsub_rn(m_prev, m_new);
+        float root = 1.f;  // the factor of l, twice
+        if (__any_sync(0xffffffffu, d != 0.f)) {
+          root = d != 0.f ? ex2(__fmul_rn(0.5f, d)) : 1.f;
+          const float a = d != 0.f ? ex2(d) : 1.f;
           // O holds the unit's tiles < gi once P.V(gi - 1) completes (s_free of
           // its buffer; see attn_rows.cuh on the parity)
           ok = mbar_wait(&sm->s_free[(gi - 1) % SB], ((gi - 1) / SB) & 1, abort_any, p.wait_ns) && ok;
@@ -591,39 +605,47 @@ __global__ void __launch_bounds__(kR8Threads, 1)
         }
         // pass 2: P over S, and this half's sum of P 2^-ev
         float half = 0.f;
+        auto pass2 = [&](auto low) {
 #pragma unroll 1
-        for (int g2 = live ? 0 : 2; g2 < 2; ++g2) {  // 32 keys
-          float v[2][16];
-          tmem_ld16(srow + 64 * wg + 32 * g2, v[0]);
-          tmem_ld16(srow + 64 * wg + 32 * g2 + 16, v[1]);
-          tmem_ld_wait_for(v[0]);
-          tmem_ld_wait_for(v[1]);
-          uint32_t w[16];
+          for (int g2 = live ? 0 : 2; g2 < 2; ++g2) {  // 32 keys
+            float v[2][16];
+            tmem_ld16(srow + 64 * wg + 32 * g2, v[0]);
+            tmem_ld16(srow + 64 * wg + 32 * g2 + 16, v[1]);
+            tmem_ld_wait_for(v[0]);
+            tmem_ld_wait_for(v[1]);
+            uint32_t w[16];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int q = 2 * g2 + h;
-            const float fq = g2 ? f[2 + h] : f[h], iq = g2 ? iv[2 + h] : iv[h];
-            const float c = __fsub_rn(g2 ? ev[2 + h] : ev[h], m_new);
+            for (int h = 0; h < 2; ++h) {
+              const int q = 2 * g2 + h;
+              const float fq = g2 ? f[2 + h] : f[h], iq = g2 ? iv[2 + h] : iv[h], evq = g2 ? ev[2 + h] : ev[h];
+              const float c = __fsub_rn(low ? fmaxf(evq, kRowEvMin) : evq, m_new);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[h][e] = ex2(__fmaf_rn(v[h][e], fq, c));
-            if (!full) {
+              for (int e = 0; e < 16; ++e) v[h][e] = ex2(__fmaf_rn(v[h][e], fq, c));
+              if (!full) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                v[h][e] = (64 * wg + 16 * q + e < nvis) ? v[h][e] : 0.f;
+                for (int e = 0; e < 16; ++e)
+                  v[h][e] = (64 * wg + 16 * q + e < nvis) ? v[h][e] : 0.f;
+              }
+              const float rest = low ? ex2(fminf(__fsub_rn(evq, kRowEvMin), 0.f)) : 1.f;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const __half2 h2 = low ? __floats2half2_rn(__fmul_rn(v[h][2 * e], rest), __fmul_rn(v[h][2 * e + 1], rest))
+                                       : __floats2half2_rn(v[h][2 * e], v[h][2 * e + 1]);
+                w[8 * h + e] = *reinterpret_cast<const uint32_t *>(&h2);
+              }
+#pragma unroll
+              for (int off = 8; off >= 1; off >>= 1)
+#pragma unroll
+                for (int e = 0; e < off; ++e) v[h][e] = __fadd_rn(v[h][e], v[h][e + off]);
+              half = __fmaf_rn(v[h][0], iq, half);
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const __half2 h2 = __floats2half2_rn(v[h][2 * e], v[h][2 * e + 1]);
-              w[8 * h + e] = *reinterpret_cast<const uint32_t *>(&h2);
-            }
-#pragma unroll
-            for (int off = 8; off >= 1; off >>= 1)
-#pragma unroll
-              for (int e = 0; e < off; ++e) v[h][e] = __fadd_rn(v[h][e], v[h][e + off]);
-            half = __fmaf_rn(v[h][0], iq, half);
+            tmem_st16(srow + 64 * wg + 32 * g2, w);
           }
-          tmem_st16(srow + 64 * wg + 32 * g2, w);
-        }
+        };
+        if (fminf(fminf(ev[0], ev[1]), fminf(ev[2], ev[3])) < kRowEvMin)  // (warp-uniform)
+          pass2(std::true_type{});
+        else
+          pass2(std::false_type{});
         if (wg == 1) sm->xsum[gi & 1][t] = half;
         const bool last = j == x.n_tiles - 1;
         if (last) {
@@ -632,14 +654,14 @@ __global__ void __launch_bounds__(kR8Threads, 1)
             break;
           }
           if (wg == 0) {
-            l_run = __fmaf_rn(l_run, a, __fadd_rn(half, sm->xsum[gi & 1][t]));
+            l_run = __fmaf_rn(__fmul_rn(l_run, root), root, __fadd_rn(half, sm->xsum[gi & 1][t]));
             // the slot of unit uo - 2 has been read by the epilogue
             ok = mbar_wait(&sm->ml_free[uo & 1], ((uo >> 1) & 1) ^ 1, abort_any, p.wait_ns) && ok;
             sm->ml[uo & 1][0][t] = m_run;
             sm->ml[uo & 1][1][t] = l_run;
           }
         } else {
-          a_prev = a;
+          root_prev = root;
           half_prev = half;
         }
         __syncwarp();

@@ -20,7 +20,13 @@
 //           at most 2^kRefTop and at least 2^kRefDrop for the largest token;
 //   O^T  += V8^T * [P_hi | P_mid | P_lo]^T, P as three 8-bit operands side by
 //           side (split_p), joined (join_p) at the split's end;
-//   l     = sum of 2^(w - ev - m) = P 2^-ev over the tokens, in fp32.
+//   l     = sum of e = 2^(w - ev - m) over the tokens, in fp32, and P = e 2^ev
+//           from it.  (The other way round, e = P 2^-ev, P is flushed to zero
+//           beside a scale 2^126 times its own, as a block of zeros may have,
+//           and the token drops out of the sum.  e is at least 2^(kRefDrop - 63)
+//           for the largest token, so what is flushed of it does not count.
+//           For the same reason a move of m scales l in two steps, and the
+//           merge's fold does: l may be 2^90, and the factor below 2^-126.)
 // (m, l, O) is a partial in the form the merge folds: out = O / l and lse =
 // (m + log2 l) ln 2.  Folding the V scale into the exponent keeps every
 // operand of one MMA on one scale, whatever the blocks' scales are, and lets
@@ -121,7 +127,7 @@ struct Q8Cfg {
     float mnew[kNP][N];                    // [buffer][row]: the reference after the pair
     __align__(16) float mw[kNW][4][N];     // [softmax warpgroup][warp][row]: the warp's copy of it
     __align__(16) float aw[kNW][4][N];     // ... and of the factor
-    float scl[kNP][N];                     // [buffer][row]: factor O and l take before it
+    float scl[kNP][N];                     // [buffer][row]: root of the factor that l takes before it
     float mrun[2][N];                      // [pair parity][row]: mnew for the next pair
     __align__(16) float rowf[kQB][N];      // [Q buffer][row]: c 2^-k
     float fin_m[N], fin_l[N];              // each row's (m, l) for the direct final write
@@ -643,7 +649,7 @@ __global__ void __launch_bounds__(32 * Q8Cfg<D, N, NSK, NSV>::kWarps, 1)
         bool ok = true;
         constexpr int kLd = 2 * N;  // S_hi and S_lo
         float sv[2][kLd];
-        float ks[2], ev[2], iv[2];
+        float ks[2], ev[2], vs[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (h == 0 || two) {
@@ -661,7 +667,7 @@ __global__ void __launch_bounds__(32 * Q8Cfg<D, N, NSK, NSV>::kWarps, 1)
           const int both = tok0 + h * kTileTokens < x.lim_max ? sm->sc[sl][t >> p.box_shift] : 127 | (127 << 8);
           ks[h] = scale_of(both & 255);
           ev[h] = static_cast<float>((both >> 8) - 127);
-          iv[h] = inv_scale_of(both >> 8);
+          vs[h] = scale_of(both >> 8);
         }
         tmem_ld_cols_wait<kLd>(sv[0]);
         if (two) tmem_ld_cols_wait<kLd>(sv[1]);
@@ -723,6 +729,7 @@ __global__ void __launch_bounds__(32 * Q8Cfg<D, N, NSK, NSV>::kWarps, 1)
         if (pi > 0)
           ok = mbar_wait_call(&sm->m_full[(pi - 1) & 1], ((pi - 1) >> 1) & 1, abort_any, p.wait_ns) && ok;
         bool moved = false;
+        float root = 1.f;
         if (lane < N) {
           const int c = lane;
           float m_new = NEG_INF, a = 1.f;
@@ -730,14 +737,18 @@ __global__ void __launch_bounds__(32 * Q8Cfg<D, N, NSK, NSV>::kWarps, 1)
             const float tmax = fmaxf(fmaxf(wmax[0][c], wmax[1][c]), fmaxf(wmax[2][c], wmax[3][c]));
             const float m_prev = j > 0 ? sm->mrun[(pi - 1) & 1][c] : NEG_INF;
             m_new = (tmax > __fadd_rn(m_prev, kRefTop)) ? __fsub_rn(tmax, kRefDrop) : m_prev;
-            a = (m_prev == NEG_INF || m_new == m_prev) ? 1.f : ex2(__fsub_rn(m_prev, m_new));
+            if (m_prev != NEG_INF && m_new != m_prev) {
+              const float d = __fsub_rn(m_prev, m_new);
+              a = ex2(d);
+              root = ex2(__fmul_rn(0.5f, d));
+              moved = true;
+            }
           }
           sm->mw[wg][wq][c] = m_new;
-          moved = a != 1.f;
           if (wq == 0) {
             sm->mrun[pi & 1][c] = m_new;
             sm->mnew[bb][c] = m_new;
-            sm->scl[bb][c] = a;
+            sm->scl[bb][c] = root;
           }
           sm->aw[wg][wq][c] = a;
         }
@@ -781,10 +792,10 @@ __global__ void __launch_bounds__(32 * Q8Cfg<D, N, NSK, NSV>::kWarps, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               float &s = sv[h][4 * q4 + i];
-              s = (s == NEG_INF) ? 0.f : ex2(__fmaf_rn(s, __fmul_rn(rfs[i], ks[h]), __fsub_rn(ev[h], ms[i])));
+              s = (s == NEG_INF) ? 0.f : ex2(__fmaf_rn(s, __fmul_rn(rfs[i], ks[h]), -ms[i]));
             }
-            const SplitP a = split_p(sv[h][4 * q4], sv[h][4 * q4 + 1]);
-            const SplitP b = split_p(sv[h][4 * q4 + 2], sv[h][4 * q4 + 3]);
+            const SplitP a = split_p(__fmul_rn(sv[h][4 * q4], vs[h]), __fmul_rn(sv[h][4 * q4 + 1], vs[h]));
+            const SplitP b = split_p(__fmul_rn(sv[h][4 * q4 + 2], vs[h]), __fmul_rn(sv[h][4 * q4 + 3], vs[h]));
             w[q4] = a.hi | (b.hi << 16);
             w[N / 4 + q4] = a.mid | (b.mid << 16);
             w[N / 2 + q4] = a.lo | (b.lo << 16);
@@ -794,15 +805,14 @@ __global__ void __launch_bounds__(32 * Q8Cfg<D, N, NSK, NSV>::kWarps, 1)
             *reinterpret_cast<uint4 *>(prow + h * C::kPTile + i * 128) =
                 make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         }
-        // the pair's row sums: p 2^-ev of both tiles, then a tree over the
+        // the pair's row sums: e of both tiles, then a tree over the
         // lanes that halves the rows a lane carries twice (six shuffles for
         // four rows); lane 8 r holds row r
 #pragma unroll
         for (int q4 = 0; q4 < N / 4; ++q4) {
           float v[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            v[e] = __fmaf_rn(sv[1][4 * q4 + e], iv[1], __fmul_rn(sv[0][4 * q4 + e], iv[0]));
+          for (int e = 0; e < 4; ++e) v[e] = __fadd_rn(sv[1][4 * q4 + e], sv[0][4 * q4 + e]);
           const bool up = lane & 16, up2 = lane & 8;
           float a0 = up ? v[2] : v[0], a1 = up ? v[3] : v[1];
           a0 = __fadd_rn(a0, __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 16));
@@ -864,7 +874,8 @@ __global__ void __launch_bounds__(32 * Q8Cfg<D, N, NSK, NSV>::kWarps, 1)
         if (t < x.rows) {
           const float lt = __fadd_rn(__fadd_rn(sm->wsum[bb][0][t], sm->wsum[bb][1][t]),
                                      __fadd_rn(sm->wsum[bb][2][t], sm->wsum[bb][3][t]));
-          l_run = __fmaf_rn(l_run, sm->scl[bb][t], lt);
+          const float root = sm->scl[bb][t];
+          l_run = __fmaf_rn(__fmul_rn(l_run, root), root, lt);
           m_run = sm->mnew[bb][t];
         }
         __syncwarp();

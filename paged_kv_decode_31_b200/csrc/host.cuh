@@ -76,11 +76,11 @@ inline size_t ws_bytes(int batch, int seqlen_q, int Hq, int D, int max_seqlen_k)
 }
 
 // Few rows (decode: rows x splits partials spread over one block per row)
-// or many (prefill, packed batches: one warp per row).
-template <int D>
+// or many (prefill, packed batches: one warp per row).  FAR: see fold_sum.
+template <int D, bool FAR = false>
 int launch_merge(const pkv::MergeParams &m, int64_t rows, cudaStream_t s) {
   if (rows <= 4096) {
-    pkv::merge_kernel<D, true><<<static_cast<unsigned>(rows), D, 0, s>>>(m);
+    pkv::merge_kernel<D, true, FAR><<<static_cast<unsigned>(rows), D, 0, s>>>(m);
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
   }
   // the warps stride over the rows: at most 8 blocks of 8 warps per SM
@@ -89,7 +89,7 @@ int launch_merge(const pkv::MergeParams &m, int64_t rows, cudaStream_t s) {
   const int64_t need = ceil_div(rows, pkv::kMergeRowsPerBlock);
   const int64_t cap = static_cast<int64_t>(sm_count(dev)) * 8;
   const int64_t blocks = need < cap ? need : cap;
-  pkv::merge_kernel<D, false><<<static_cast<unsigned>(blocks), 32 * pkv::kMergeRowsPerBlock, 0, s>>>(m);
+  pkv::merge_kernel<D, false, FAR><<<static_cast<unsigned>(blocks), 32 * pkv::kMergeRowsPerBlock, 0, s>>>(m);
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 

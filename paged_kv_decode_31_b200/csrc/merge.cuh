@@ -63,6 +63,15 @@ __device__ __forceinline__ FoldCoef fold_coef(float M, float m_s) {
 __device__ __forceinline__ float fold_val(float X, float x_s, const FoldCoef &k) {
   return __fmaf_rn(x_s, k.c, __fmul_rn(X, k.a));
 }
+// The sums.  m of an 8-bit cache's partial holds the V scales (attn_split_q8.cuh)
+// and l is that much larger where they are small, to 2^90: a factor below 2^-126,
+// flushed to zero, is then applied as its root, twice.  (A bf16 cache's l lies
+// between 1 and 2^20 and does not need it: FAR is false there.)
+__device__ __forceinline__ float fold_sum(float M, float L, float m_s, float l_s, const FoldCoef &k) {
+  if (M == __int_as_float(0xff800000) || fminf(k.a, k.c) > 0.f) return fold_val(L, l_s, k);
+  const float root = ex2(__fmul_rn(-0.5f, fabsf(__fsub_rn(M, m_s))));
+  return k.c > 0.f ? __fmaf_rn(__fmul_rn(L, root), root, l_s) : __fmaf_rn(__fmul_rn(l_s, root), root, L);
+}
 // Final write of a folded row: out element and lse.  out = A / L rounded to
 // nearest (the IEEE quotient), from the row's reciprocal rL = final_rcp(L),
 // taken once per row, by two residual corrections:
@@ -106,7 +115,7 @@ __device__ __forceinline__ float final_lse(float M, float L) {
 //                 splits: more SMs share the partial reads).
 // One output row (row = token * Hq + h; token = b * seqlen_q + i, or packed)
 // by one block (WIDE) or one warp; `lane` is the thread's index in it.
-template <int D, bool WIDE>
+template <int D, bool WIDE, bool FAR>
 __device__ __forceinline__ void merge_row(const MergeParams &p, int64_t row, int lane) {
   constexpr int V = WIDE ? 1 : D / 32;
   const int h = static_cast<int>(row % p.Hq);
@@ -169,7 +178,7 @@ __device__ __forceinline__ void merge_row(const MergeParams &p, int64_t row, int
     for (int k = 0; k < kBatch; ++k) {
       if (ms[k] == NEG_INF) continue;  // the row sees no key of this split
       const FoldCoef kc = fold_coef(M, ms[k]);
-      L = fold_val(L, ls[k], kc);
+      L = FAR ? fold_sum(M, L, ms[k], ls[k], kc) : fold_val(L, ls[k], kc);
 #pragma unroll
       for (int j = 0; j < V; ++j) A[j] = fold_val(A[j], as[k][j], kc);
       M = kc.Mn;
@@ -198,16 +207,16 @@ __device__ __forceinline__ void merge_row(const MergeParams &p, int64_t row, int
 // WIDE: one block per row.  Otherwise one warp per row, the warps of the grid
 // striding over the rows (a few blocks per SM: most rows of a packed call may
 // only need the check that the row-major kernel finished them).
-template <int D, bool WIDE>
+template <int D, bool WIDE, bool FAR>
 __global__ void __launch_bounds__(WIDE ? D : 32 * kMergeRowsPerBlock)
     merge_kernel(const __grid_constant__ MergeParams p) {
   if constexpr (WIDE) {
-    if (static_cast<int64_t>(blockIdx.x) < p.rows) merge_row<D, true>(p, blockIdx.x, threadIdx.x);
+    if (static_cast<int64_t>(blockIdx.x) < p.rows) merge_row<D, true, FAR>(p, blockIdx.x, threadIdx.x);
   } else {
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kMergeRowsPerBlock;
     for (int64_t row = static_cast<int64_t>(blockIdx.x) * kMergeRowsPerBlock + (threadIdx.x >> 5);
          row < p.rows; row += stride)
-      merge_row<D, false>(p, row, threadIdx.x & 31);
+      merge_row<D, false, FAR>(p, row, threadIdx.x & 31);
   }
 }
 

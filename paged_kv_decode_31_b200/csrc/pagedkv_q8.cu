@@ -314,7 +314,7 @@ int attn_q8_entry(const void *q, const int64_t q_strides[3], const void *k_cache
   m.skip_single = split_only ? 0 : 1;
   m.skip_min_nq = both ? small_nq + 1 : 0;
   m.n_local = static_cast<int>(S);
-  return D == 128 ? launch_merge<128>(m, rows, s) : launch_merge<64>(m, rows, s);
+  return D == 128 ? launch_merge<128, true>(m, rows, s) : launch_merge<64, true>(m, rows, s);
 }
 
 }  // namespace
