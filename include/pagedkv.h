@@ -454,9 +454,10 @@ int pkv_rope(const void *q, const int64_t q_strides[3], void *q_out, const int64
  * otherwise packed, [total_new, heads, D] with the last two of the strides
  * used, sequence b owning cu_seqlens_new[b] .. cu_seqlens_new[b+1] - 1.  Tokens
  * behind cu_seqlens_new[batch] are left alone.  Two sequences must not share a
- * block that the call writes, nor may a table name one twice there.  Errors and device error bits as pkv_kv_append;
- * a range of cu_seqlens_new that decreases or leaves [0, total_new] sets
- * PKV_DEVERR_QUERY_LEN and is skipped.
+ * block that the call writes, nor may a table name one twice there.  Errors and
+ * device error bits as pkv_kv_append; a range of cu_seqlens_new that decreases
+ * or leaves [0, total_new] sets PKV_DEVERR_QUERY_LEN and is skipped, and tokens
+ * of other sequences may be skipped with it.
  */
 int pkv_kv_append_rope(const void *q, const int64_t q_strides[3], void *q_out, const int64_t qo_strides[3],
                        int Hq, const void *k_new, const int64_t kn_strides[3], const void *v_new,

@@ -297,6 +297,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
     const int64_t y = x / p.cluster;
     const int per = (p.Hkv + p.heads - 1) / p.heads;  // head groups
     append_block_q8<P>(p, y / per, static_cast<int>(y % per) * p.heads, static_cast<int>(x % p.cluster));
+  } else if (p.r.cu && x == gridDim.x - 1) {
+    check_ranges(p.r);  // (a block of its own, behind the queries')
   } else if (p.r.x[0].heads > 0) {
     const int warp = threadIdx.x >> 5;
     rope_warp(p.r, (x - p.kv_blocks) * kRopeWarps + warp, cs[warp]);

@@ -53,7 +53,7 @@ void rope_chunks(RopeParams *p) {
 int launch_rope(RopeParams &p, cudaStream_t s) {
   if (p.tokens == 0) return PKV_OK;
   rope_chunks(&p);
-  const int64_t blocks = ceil_div(p.tokens * p.chunks, kRopeWarps);
+  const int64_t blocks = ceil_div(p.tokens * p.chunks, kRopeWarps) + (p.cu ? 1 : 0);  // (and check_ranges)
   if (blocks > INT32_MAX) return PKV_ERR_ARG;
   rope_kernel<<<static_cast<unsigned>(blocks), kRopeThreads, 0, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
@@ -205,7 +205,8 @@ int pkv_kv_append_q8(const void *q, const int64_t q_strides[3], void *q_out, con
   a.kv_blocks = a.groups * ceil_div(Hkv, a.heads) * a.cluster;
   p.chunks = 1;
   if (p.x[0].heads) rope_chunks(&p);
-  int64_t blocks = a.kv_blocks + (p.x[0].heads ? ceil_div(p.tokens * p.chunks, kRopeWarps) : 0);
+  int64_t blocks = a.kv_blocks + (p.x[0].heads ? ceil_div(p.tokens * p.chunks, kRopeWarps) : 0) +
+                   (p.cu ? 1 : 0);  // (check_ranges)
   blocks = ceil_div(blocks, a.cluster) * a.cluster;  // (a warp past the last query row returns at once)
   if (blocks > INT32_MAX) return PKV_ERR_ARG;
   cudaLaunchAttribute attr{};

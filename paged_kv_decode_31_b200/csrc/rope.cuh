@@ -147,6 +147,12 @@ __device__ __forceinline__ int2 packed_range(const int32_t *cu, int b, int64_t t
   return bad ? make_int2(0, 0) : make_int2(a, e - a);
 }
 
+// Every range of a packed call, by the threads of one block.  (The search for a
+// token's sequence does not pass by all of them when they do not ascend.)
+__device__ __forceinline__ void check_ranges(const RopeParams &p) {
+  for (int b = threadIdx.x; b < p.batch; b += kRopeThreads) packed_range(p.cu, b, p.tokens, p.err);
+}
+
 __device__ __forceinline__ RopeToken rope_token(const RopeParams &p, int64_t r) {
   RopeToken k{};
   int b, t;
@@ -249,8 +255,14 @@ __device__ __forceinline__ void rope_warp(const RopeParams &p, int64_t item, flo
   }
 }
 
+// Packed calls have a last block that only looks at the ranges (beside the others:
+// no token's rows wait for it).
 __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_constant__ RopeParams p) {
   __shared__ __align__(16) float2 cs[kRopeWarps][64];
+  if (p.cu && blockIdx.x == gridDim.x - 1) {
+    check_ranges(p);
+    return;
+  }
   const int warp = threadIdx.x >> 5;
   rope_warp(p, static_cast<int64_t>(blockIdx.x) * kRopeWarps + warp, cs[warp]);
 }
