@@ -24,15 +24,17 @@ int make_kv_map_q8(CUtensorMap *map, const void *base, const int64_t st[3], int6
                    int block_size, int Hkv, int D, int box_slots, int *head_first) {
   auto enc = encode_fn();
   if (!enc) return PKV_ERR_CUDA;
-  const bool hf = st[2] <= st[1];
+  // (one head: its axis is never stepped over, its stride says nothing)
+  const bool hf = Hkv > 1 && st[2] <= st[1];
+  const int64_t head = Hkv > 1 ? st[2] : st[1];
   cuuint64_t dims[4], strides[3];
   cuuint32_t box[4], estr[4] = {1, 1, 1, 1};
   dims[0] = static_cast<cuuint64_t>(D);
   dims[1] = static_cast<cuuint64_t>(hf ? Hkv : block_size);
   dims[2] = static_cast<cuuint64_t>(hf ? block_size : Hkv);
   dims[3] = static_cast<cuuint64_t>(num_blocks);
-  strides[0] = static_cast<cuuint64_t>(hf ? st[2] : st[1]);
-  strides[1] = static_cast<cuuint64_t>(hf ? st[1] : st[2]);
+  strides[0] = static_cast<cuuint64_t>(hf ? head : st[1]);
+  strides[1] = static_cast<cuuint64_t>(hf ? st[1] : head);
   strides[2] = static_cast<cuuint64_t>(st[0]);
   box[0] = static_cast<cuuint32_t>(D);
   box[1] = static_cast<cuuint32_t>(hf ? 1 : box_slots);
