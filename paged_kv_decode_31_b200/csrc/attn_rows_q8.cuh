@@ -23,17 +23,19 @@
 // leaves TMEM for a third S buffer.  V is widened because P in fp16 needs an
 // fp16 partner; K is read in place.
 //
-// What bounds it: issue slots and the instruction cache.  8 x 512 queries at
-// context 2048, Hq 16 / Hkv 4, D 128: 136 us, 442 TFLOP/s; 3300 cycles a tile,
-// of which the softmax's two passes take 2100; tensor pipe 23 %, instruction-
-// cache hits 86 %.
-// Code that stays small is what made it fast (start: 175 us): rolled softmax
-// loops (-16), query rows converted a few at a time between V tiles and an
-// epilogue of rolled 16-column steps without registers of its own for O, which
-// also leaves the softmax 128 registers (-24).  Measured and dropped: the two
-// softmax warpgroups on alternate tiles (equal), 16 keys in flight ahead of
-// those in use (+22), S kept in registers between the passes (+32), either
-// pass unrolled (+2, +5), scales read inside the loops (+6).
+// What bounds it: the length of a tile's chain, not a unit of the SM.  8 x 512
+// queries at context 2048, Hq 16 / Hkv 4, D 128: 139.6 us, 430 TFLOP/s; 3300
+// cycles a tile, of which the softmax's two passes take 2100, the exchange of
+// the halves' maxima 120 and waits for S and the scale bytes 900, while the
+// tensor pipe is at 23 %, issue at 48 % and the exponential pipe at 20 %: with
+// one tile of rows per CTA nothing else runs beside its softmax.
+// Code that stays small is what made it fast (start: 175 us; instruction-cache
+// hits 70 % then, 86 % now): rolled softmax loops (-16), query rows converted a
+// few at a time between V tiles and an epilogue of rolled 16-column steps without
+// registers of its own for O, which also leaves the softmax 128 registers (-24).
+// Measured and dropped: the two softmax warpgroups on alternate tiles (equal),
+// 16 keys in flight ahead of those in use (+22), S kept in registers between the
+// passes (+32), either pass unrolled (+2, +5), scales read inside the loops (+6).
 //
 // Roles (640 threads): warps 0-3 / 4-7 softmax (thread t = row t, keys [0, 64)
 // and [64, 128) of every tile), 8-11 epilogue, 12-15 converters (V to fp16, and
@@ -57,8 +59,8 @@ constexpr float kRowDrop = 7.f;
 // through the exponential with 2^kRowEvMin in its place, and P gets the rest
 // afterwards.  What is flushed then is below 2^-102 of l's units, 2^-90 for a
 // split's 4096 tokens, and l at least 2^(kRowDrop - 63).  (The form of
-// attn_split_q8.cuh costs a product per element here, issue slots that this
-// kernel does not have: 146 us instead of 139.6 for 8 x 512 queries.)
+// attn_split_q8.cuh costs a product per element in the longest part of the
+// chain: 146 us instead of 139.6 for 8 x 512 queries.)
 constexpr float kRowEvMin = -24.f;
 // Registers per thread: at launch, and each warpgroup's share of their sum.
 constexpr int kR8LaunchRegs = 96, kR8SoftmaxRegs = 128, kR8EpiRegs = 88, kR8ConvRegs = 72, kR8AuxRegs = 64;

@@ -38,10 +38,14 @@
 // place the tensor cores and the shared memory see no conversion traffic
 // (widening the tile to bf16 in shared memory would move 5 bytes per cache byte
 // through it).  4 x 131072 tokens in 16-token blocks, 4 rows per KV head: 197
-// us, 5.45 TB/s (the loads alone: 188, a box of 16 rows at a time); 64 contexts
-// up to 32768 in 256-token blocks: 185 us, 5.57 TB/s.  With more rows per unit
-// the softmax takes over: 8 rows 4.6 TB/s, 16 rows 2.8 TB/s (7400 cycles a pair
-// of tiles; still ahead of the row-major kernel's 1.7 TB/s at 16 rows).
+// to 199.5 us from device to device, 5.4 TB/s (the loads alone: 188, a box of 16
+// rows at a time); 64 contexts up to 32768 in 256-token blocks: 185 us, 5.57
+// TB/s.  With more rows per unit the latency of the softmax takes over -- two
+// warpgroups that pass the reference on from pair to pair, a thread's scores
+// past its registers (64 bytes spilled for 8 rows, 212 for 16) -- and no unit of
+// the SM is full: 64 x 16384 tokens with 8 rows per KV head 221 us, 4.9 TB/s,
+// with 16 rows 379 us, 2.8 TB/s (7400 cycles a pair of tiles; still ahead of the
+// row-major kernel's 1.7 TB/s at 16 rows).
 #pragma once
 
 #include "attn_split.cuh"
@@ -372,7 +376,7 @@ __device__ __forceinline__ void load_q8(const Q8Params &p, const CUtensorMap *ma
                                         typename C::Small *sm, uint64_t *full, uint64_t *empty,
                                         uint32_t dst_off, bool is_k, int part, int lane,
                                         volatile int *abort_any, const Sched8 &sc) {
-  constexpr int D = C::kD, N = C::kN, US = C::kUS;
+  constexpr int D = C::kD, US = C::kUS;
   const int bmask = (1 << p.block_shift) - 1;
   if (lane == 0) tma_prefetch_desc(map);
   const uint32_t box_bytes = static_cast<uint32_t>(p.box_slots * D);

@@ -83,9 +83,13 @@ __device__ __forceinline__ float fold_sum(float M, float L, float m_s, float l_s
 // the IBM RISC System/6000 processor", IBM J. Res. Dev. 34(1), 1990; J.-M.
 // Muller et al., Handbook of Floating-Point Arithmetic, division with an
 // FMA).  The theorem needs every intermediate in the normal range:
-// final_fast_ok holds for |A| in [2^-90, 2^96] and L in [2^-20, 2^40] (a row
-// that saw a key has L >= 1), and for A = +-0, whose quotient is A rL itself;
-// other operands (subnormal, infinite or NaN A) take the IEEE division.
+// final_fast_ok holds for |A| in [2^-90, 2^96] and L in [2^-20, 2^40], and for
+// A = +-0, whose quotient is A rL itself; other operands (subnormal, infinite or
+// NaN A) take the IEEE division.  A row that saw a key has L >= 1 over a bf16
+// cache.  Over an 8-bit one its tokens count 2^-ev for a V scale of 2^ev, the
+// largest 2^7 times that or more, so L may lie anywhere from 2^-56 to 2^95: V of
+// about 1 has ev = -6 and L up to 2^38, rows of much smaller or larger V take
+// the division.
 // Either way the bits are __fdiv_rn(A, L)'s.
 __device__ __forceinline__ float final_rcp(float L) { return L > 0.f ? __frcp_rn(L) : 0.f; }
 __device__ __forceinline__ bool final_fast_ok(float A, float L) {

@@ -160,24 +160,12 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Read-only loads that stay where they are written: a plain load may be moved
+// A read-only load that stays where it is written: a plain load may be moved
 // down to its use by the compiler, and then no longer runs ahead of the work
 // between.
-__device__ __forceinline__ int ldg_here(const int *p) {
-  int v;
-  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(p));
-  return v;
-}
 __device__ __forceinline__ int ldg_here(const uint8_t *p) {
   int v;
   asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v) : "l"(p));
-  return v;
-}
-__device__ __forceinline__ uint4 ldg_here(const uint4 *p) {
-  uint4 v;
-  asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
   return v;
 }
 
@@ -302,19 +290,6 @@ __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_
       : "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem desc], kind::f8f6f4.  A (M x 32, 8 bits) sits
-// in TMEM: lane m holds row m, 32-bit column c holds elements 4c .. 4c + 3 of
-// K, the first in the lowest byte.  Issued by a single thread.
-__device__ __forceinline__ void umma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                           uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // Arrive (once) on `bar` when every tcgen05 operation this thread issued so
 // far has completed.
 __device__ __forceinline__ void umma_commit(uint64_t *bar) {
@@ -375,8 +350,6 @@ __device__ __forceinline__ void tmem_ld_wait_for8(float *v) {
                : "memory");
 }
 
-// Each thread of the warp writes 16 consecutive 32-bit columns of its own
-// TMEM lane (the mirror of tmem_ld16).
 // Programmatic dependent launch.  launch_dependents: a grid launched to overlap
 // this one may start once every CTA of this grid has got here (or ended).
 // wait: the grids before this one are complete and their writes visible; at
@@ -384,6 +357,8 @@ __device__ __forceinline__ void tmem_ld_wait_for8(float *v) {
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_grids_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Each thread of the warp writes 16 consecutive 32-bit columns of its own
+// TMEM lane (the mirror of tmem_ld16).
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
