@@ -523,10 +523,12 @@ int pkv_kv_append_q8(const void *q, const int64_t q_strides[3], void *q_out, con
  * scale <= 8.  q stays bf16 and out bf16; sums and softmax statistics are
  * fp32.  A query row takes part as two 8-bit operands that add up to it (to
  * 2^-21 of its largest element or exactly; rows whose largest magnitude is
- * above 2^67 saturate), a probability rounded to fp16 (as three 8-bit operands
+ * above 2^67 saturate, below 2^-53 they keep fewer bits), a probability rounded to fp16 (as three 8-bit operands
  * that add up to that, or as one fp16 operand) on a scale that holds a row's
  * largest of every 4096 tokens at 2^7 or more: off by 2^-11 of itself, or by
- * 2^-32 of that largest where that is more (below 2^-21 of it).
+ * 2^-32 of that largest where that is more (below 2^-21 of it).  "Largest" is by
+ * p times its block's V scale.  The scales of a row's blocks may lie anywhere in
+ * [-63, 63] beside each other: the sum counts every token at its own weight.
  * A request of n query tokens with n * Hq / Hkv <= 16 rows per KV head is
  * computed by one kernel, larger ones by another (their sums round in another
  * order); in a packed call each request's own n decides.  Within either, for a

@@ -22,7 +22,7 @@
 // What bounds it: bytes (2 read, 1 written per value) and the latency of one
 // pass: table, scales, rows, maxima, stores, each waiting for the one before.
 // 24 prompts of up to 1024 tokens, 16 query and 4 KV heads of 128, 64-token
-// blocks: 36 us, 3.0 TB/s; a token for each of 64 sequences: 6 us.
+// blocks: 36 to 38 us, 2.9 TB/s; a token for each of 64 sequences: 6 us.
 #pragma once
 
 #include "f8.cuh"

@@ -27,10 +27,10 @@
 // queries at context 2048, Hq 16 / Hkv 4, D 128: 139.6 us, 430 TFLOP/s; 3300
 // cycles a tile, of which the softmax's two passes take 2100, the exchange of
 // the halves' maxima 120 and waits for S and the scale bytes 900, while the
-// tensor pipe is at 23 %, issue at 48 % and the exponential pipe at 20 %: with
+// tensor pipe is at 23 %, issue at 49 % and the exponential pipe at 24 %: with
 // one tile of rows per CTA nothing else runs beside its softmax.
 // Code that stays small is what made it fast (start: 175 us; instruction-cache
-// hits 70 % then, 86 % now): rolled softmax loops (-16), query rows converted a
+// hits 71 % then, 84 % now): rolled softmax loops (-16), query rows converted a
 // few at a time between V tiles and an epilogue of rolled 16-column steps without
 // registers of its own for O, which also leaves the softmax 128 registers (-24).
 // Measured and dropped: the two softmax warpgroups on alternate tiles (equal),

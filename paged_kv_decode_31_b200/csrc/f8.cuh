@@ -3,7 +3,8 @@
 // splits that let 8-bit tensor-core operands carry 16-bit values.
 //
 // The cache holds e4m3 values; a value's block and KV head have a scale 2^e,
-// kept as the byte e + 127 (E8M0), with e in [kScaleExpMin, kScaleExpMax].
+// kept as the byte e + 127 (E8M0), with e in [kScaleExpMin, kScaleExpMax].  The
+// attention kernels take any two of these beside each other in one row.
 #pragma once
 
 #include <cuda_fp16.h>
